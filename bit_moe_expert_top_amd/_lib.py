@@ -65,6 +65,9 @@ _SIGS = {
     "moe_expert_ffn_ws_region": (_i32, [ctypes.POINTER(MoeWeights), _i32, _i32, _sz, _i32,
                                         ctypes.POINTER(_sz), ctypes.POINTER(_sz)]),
     "moe_fp8_slot_layout": (_i32, [_i32, _i32] + [ctypes.POINTER(_sz)] * 5),
+    "moe_add_rmsnorm": (_i32, [_p, _i32, _p, _i32, _p, ctypes.c_float, _i32, _i32, _p, _p, _p, _p, _p]),
+    "moe_linear": (_i32, [_p] * 4 + [_i32] * 4 + [_p, _i32, _p, _i32, _p, _i32, _p]),
+    "moe_route_scored": (_i32, [_p, _p] + [_i32] * 8 + [ctypes.c_float, _p, _p, _p]),
     "moe_status_str": (ctypes.c_char_p, [_i32]),
     "moe_tier_plan": (_i32, [ctypes.POINTER(MoeTierState), _p, _i64, _p, _p, _p]),
     "moe_tier_load": (_i32, [ctypes.POINTER(MoeWeights), ctypes.POINTER(MoeWeights), _p, _p, _i32, _p]),
@@ -353,6 +356,161 @@ def layer_forward(w: DeviceWeights, logits: torch.Tensor, x: torch.Tensor, k: in
     y = moe_expert_ffn(w, x, k, counts, offsets, perm, fp8_slots=fp8_slots)
     out = moe_combine(y, inv, gw, out_fp32=out_fp32)
     return dict(ids=ids, gates=gw, counts=counts, offsets=offsets, perm=perm, inv=inv, y_perm=y, out=out)
+
+
+# --------------------------------------------------------------------- around the expert FFN
+MOE_DT_F32, MOE_DT_BF16, MOE_DT_MXFP8 = 1, 2, 3
+ACTS = {"none": 0, "relu": 1, "gelu": 2, "silu": 3, "swiglu": 4}
+SCORES = {"softmax": 1, "sigmoid": 2}
+# bf16 arrays are given as bfloat16 tensors or as their bits (int16), e4m3fn elements and e8m0
+# scales as tensors of those types or as bytes
+_FLOAT_DT = {torch.float32: MOE_DT_F32, torch.bfloat16: MOE_DT_BF16, torch.int16: MOE_DT_BF16}
+_BF16 = (torch.bfloat16, torch.int16)
+_E4M3 = (torch.uint8, torch.float8_e4m3fn)
+_E8M0 = (torch.uint8, torch.float8_e8m0fnu)
+
+
+def _arg(t, dtypes, shape, dev, name: str):
+    """The device pointer of an argument, checked; None for None."""
+    if t is None:
+        return None
+    if t.dtype not in dtypes or t.shape != shape or t.device != dev or not t.is_contiguous():
+        raise ValueError(f"{name}: expected a contiguous {' or '.join(map(str, dtypes))} tensor of shape "
+                         f"{tuple(shape)} on {dev}, got {t.dtype} {tuple(t.shape)} on {t.device}"
+                         f"{'' if t.is_contiguous() else ' (not contiguous)'}")
+    return t.data_ptr()
+
+
+def _call_on(dev, fn: str, *args):
+    """Enqueue a library call on the current stream of the tensors' device."""
+    if dev.type != "cuda":
+        raise ValueError(f"{fn}: expected tensors on the GPU, got {dev}")
+    if dev.index == torch.cuda.current_device():
+        _check(fn, getattr(lib, fn)(*args, _stream()))
+    else:
+        with torch.cuda.device(dev):
+            _check(fn, getattr(lib, fn)(*args, _stream()))
+
+
+def moe_add_rmsnorm(x: torch.Tensor, weight: torch.Tensor, eps: float, residual=None, residual_out=None, y=None,
+                    q=None, q_scales=None):
+    """s = x + residual; y = s * weight / sqrt(mean(s^2) + eps), in bf16 and/or as MXFP8 (q, q_scales).
+    x: fp32 or bf16 [T][H]; residual: fp32 or bf16 or None; the outputs are written to the tensors given
+    (residual_out may be residual; y defaults to a new tensor if no q is given).  Returns y (None if not
+    asked for)."""
+    dev = x.device
+    if x.dim() != 2 or x.dtype not in _FLOAT_DT or not x.is_contiguous():
+        raise ValueError("x: expected a contiguous float32 or bf16 tensor [T][H]")
+    shape = x.shape
+    T, H = shape
+    if y is None and q is None:
+        y = torch.empty(shape, dtype=torch.int16, device=dev)
+    if (q is None) != (q_scales is None):
+        raise ValueError("q and q_scales go together")
+    if residual is None and residual_out is not None:
+        raise ValueError("residual_out without a residual")
+    pr, rd = None, MOE_DT_BF16
+    if residual is not None:
+        pr, rd = _arg(residual, tuple(_FLOAT_DT), shape, dev, "residual"), _FLOAT_DT[residual.dtype]
+    pro = None
+    if residual_out is not None:
+        pro = _arg(residual_out, (torch.float32,) if rd == MOE_DT_F32 else _BF16, shape, dev, "residual_out")
+    _call_on(dev, "moe_add_rmsnorm", x.data_ptr(), _FLOAT_DT[x.dtype], pr, rd,
+             _arg(weight, _BF16, (H,), dev, "weight"), eps, T, H, pro, _arg(y, _BF16, shape, dev, "y"),
+             _arg(q, _E4M3, shape, dev, "q"), _arg(q_scales, _E8M0, (T, H // 32), dev, "q_scales"))
+    return y
+
+
+def moe_linear(x: torch.Tensor, w: torch.Tensor, x_scales=None, w_scales=None, bias=None, act: str = "none",
+               residual=None, out=None, out_dtype=torch.int16):
+    """out = act(x W^T + bias) + residual.  x [T][K] and w [N][K] are bf16, or MXFP8 elements with their
+    scales; bias fp32 [N]; act one of ACTS (swiglu: the first half of w's rows is the gate, N/2 columns
+    out); residual and out fp32 or bf16 (out may be residual)."""
+    dev = x.device
+    if x.dim() != 2 or w.dim() != 2 or act not in ACTS:
+        raise ValueError(f"moe_linear: expected x [T][K], w [N][K] and an act of {sorted(ACTS)}")
+    T, K = x.shape
+    N = w.shape[0]
+    mx = x_scales is not None
+    if mx != (w_scales is not None):
+        raise ValueError("x_scales and w_scales go together")
+    kinds = _E4M3 if mx else _BF16
+    cols = N // 2 if act == "swiglu" else N
+    if out is None:
+        out = torch.empty((T, cols), dtype=out_dtype, device=dev)
+    if out.dtype not in _FLOAT_DT:
+        raise ValueError("out: expected float32 or bf16")
+    pr, rd = None, MOE_DT_F32
+    if residual is not None:
+        pr, rd = _arg(residual, tuple(_FLOAT_DT), (T, cols), dev, "residual"), _FLOAT_DT[residual.dtype]
+    _call_on(dev, "moe_linear", _arg(x, kinds, (T, K), dev, "x"), _arg(x_scales, _E8M0, (T, K // 32), dev, "x_scales"),
+             _arg(w, kinds, (N, K), dev, "w"), _arg(w_scales, _E8M0, (N, K // 32), dev, "w_scales"),
+             MOE_DT_MXFP8 if mx else MOE_DT_BF16, T, N, K, _arg(bias, (torch.float32,), (N,), dev, "bias"), ACTS[act],
+             pr, rd, _arg(out, (out.dtype,), (T, cols), dev, "out"), _FLOAT_DT[out.dtype])
+    return out
+
+
+def moe_route_scored(logits: torch.Tensor, k: int, score: str = "softmax", bias=None, n_group: int = 1,
+                     topk_group: int = 1, group_top: int = 1, renormalize: bool = False, scale: float = 1.0,
+                     topk_ids=None, topk_w=None):
+    """Top-k of softmax or sigmoid scores with a bias for the choice and group-limited selection; the
+    gates are the unbiased scores, renormalised if asked for, times scale."""
+    dev = logits.device
+    if logits.dim() != 2 or score not in SCORES:
+        raise ValueError(f"moe_route_scored: expected logits [T][E] and a score of {sorted(SCORES)}")
+    T, E = logits.shape
+    topk_ids = torch.empty((T, k), dtype=torch.int32, device=dev) if topk_ids is None else topk_ids
+    topk_w = torch.empty((T, k), dtype=torch.float32, device=dev) if topk_w is None else topk_w
+    _call_on(dev, "moe_route_scored", _arg(logits, (torch.float32,), (T, E), dev, "logits"),
+             _arg(bias, (torch.float32,), (E,), dev, "bias"), T, E, k, SCORES[score], n_group, topk_group, group_top,
+             1 if renormalize else 0, scale, _arg(topk_ids, (torch.int32,), (T, k), dev, "topk_ids"),
+             _arg(topk_w, (torch.float32,), (T, k), dev, "topk_w"))
+    return topk_ids, topk_w
+
+
+class MoeBlock:
+    """A MoE block around one layer's routed experts: norm weight, router (weight, bias for balance and
+    the arguments of moe_route_scored) and an optional shared expert, bf16 (ws1 [2Is][H], ws2 [H][Is]) or
+    MXFP8 (ws1 and ws2 as pairs (elements, scales))."""
+
+    def __init__(self, experts: DeviceWeights, k: int, norm_weight, router_weight, eps: float = 1e-6,
+                 router_bias=None, route: dict | None = None, ws1=None, ws2=None):
+        if (ws1 is None) != (ws2 is None):
+            raise ValueError("ws1 and ws2 go together")
+        self.experts, self.k, self.eps = experts, k, eps
+        self.norm_weight, self.router_weight, self.router_bias = norm_weight, router_weight, router_bias
+        self.route = dict(route or {})
+        self.ws1, self.ws2 = ws1, ws2
+
+
+def block_forward(blk: MoeBlock, x: torch.Tensor, residual: torch.Tensor):
+    """One MoE block of a pre-norm residual stream: x (the previous sublayer's output, fp32 or bf16) joins
+    the residual stream in place, its norm is routed and run through the experts and the shared expert.
+    Returns every intermediate; ``out`` is the block's output (fp32, or bf16 with an MXFP8 shared expert),
+    to be added to ``residual`` by the next norm."""
+    w, dev = blk.experts, x.device
+    T, H = x.shape
+    mx = isinstance(blk.ws1, tuple)
+    with torch.cuda.device(dev):
+        y = torch.empty((T, H), dtype=torch.int16, device=dev)
+        q = torch.empty((T, H), dtype=torch.uint8, device=dev) if mx else None
+        qs = torch.empty((T, H // 32), dtype=torch.uint8, device=dev) if mx else None
+        moe_add_rmsnorm(x, blk.norm_weight, blk.eps, residual=residual, residual_out=residual, y=y, q=q, q_scales=qs)
+        logits = moe_linear(y, blk.router_weight, out_dtype=torch.float32)
+        ids, gates = moe_route_scored(logits, blk.k, bias=blk.router_bias, **blk.route)
+        counts, offsets, perm, inv = moe_permute(ids, w.E)
+        y_perm = moe_expert_ffn(w, y, blk.k, counts, offsets, perm)
+        out = routed = moe_combine(y_perm, inv, gates, out_fp32=True)
+        h = None
+        if mx:
+            h = moe_linear(q, blk.ws1[0], x_scales=qs, w_scales=blk.ws1[1], act="swiglu")
+            hq, hs = moe_mxfp8_quantize(h)
+            out = moe_linear(hq, blk.ws2[0], x_scales=hs, w_scales=blk.ws2[1], residual=routed)
+        elif blk.ws1 is not None:
+            h = moe_linear(y, blk.ws1, act="swiglu")
+            out = moe_linear(h, blk.ws2, residual=routed, out_dtype=torch.float32)
+    return dict(y=y, q=q, q_scales=qs, logits=logits, ids=ids, gates=gates, counts=counts, offsets=offsets, perm=perm,
+                inv=inv, y_perm=y_perm, routed=routed, h=h, out=out)
 
 
 # --------------------------------------------------------------------- host-RAM expert tier

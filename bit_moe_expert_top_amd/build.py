@@ -1,7 +1,7 @@
 """Build the HIP library ``libbitmoe.so`` in-tree with hipcc for gfx950.
 
 ``python -m bit_moe_expert_top_amd.build`` (or ``build()``) compiles every source under
-``csrc/`` and links the shared library next to this file.
+``csrc/`` (the expert layer) and ``csrc/block/`` (the operators around it) and links the shared library next to this file.
 """
 from __future__ import annotations
 
@@ -12,6 +12,7 @@ import sys
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
+BLOCK = os.path.join(CSRC, "block")
 OBJ = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libbitmoe.so")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
@@ -26,7 +27,7 @@ FLAGS = [
 
 
 def sources():
-    return sorted(os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".hip", ".cpp")))
+    return sorted(os.path.join(d, f) for d in (CSRC, BLOCK) for f in os.listdir(d) if f.endswith((".hip", ".cpp")))
 
 
 def _compile(src: str) -> str:

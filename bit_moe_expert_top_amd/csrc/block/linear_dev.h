@@ -1,0 +1,88 @@
+// The epilogue of the dense product, shared by its kernels.
+#pragma once
+
+#include "../common.h"
+#include "block_kernels.h"
+
+namespace bitmoe {
+
+typedef float f32x16_t __attribute__((ext_vector_type(16)));
+
+// D(32x32, f32) += A(32x16, bf16) * B(16x32, bf16): lane l supplies A row l % 32 and B column l % 32
+// for k = 8 (l / 32) .. + 7 and receives D[8 (j / 4) + 4 (l / 32) + j % 4][l % 32] in register j.
+__device__ __forceinline__ f32x16_t mfma_bf16_32x32x16(u32x4 a, u32x4 b, f32x16_t c) {
+  return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0,
+                                                 0, 0);
+}
+// The same with e4m3 operands of 64 k and e8m0 scales per 32 k: lane l (half h = l / 32) supplies k = 32 c + 16 h
+// + [0, 16) in its 16-byte chunks c = 0, 1 and the scale byte of the 32-k block h.
+__device__ __forceinline__ f32x16_t mfma_mxfp8_32x32x64(u32x4 a0, u32x4 a1, u32x4 b0, u32x4 b1, f32x16_t c,
+                                                        uint32_t sa, uint32_t sb) {
+  const i32x8 a = {(int)a0[0], (int)a0[1], (int)a0[2], (int)a0[3], (int)a1[0], (int)a1[1], (int)a1[2], (int)a1[3]};
+  const i32x8 b = {(int)b0[0], (int)b0[1], (int)b0[2], (int)b0[3], (int)b1[0], (int)b1[1], (int)b1[2], (int)b1[3]};
+  return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a, b, c, 0, 0, 0, (int)sa, 0, (int)sb);
+}
+
+// The activations in fp32 (each a few ulp).  exp overflows to inf for very negative arguments,
+// where the quotient is the right limit 0.
+__device__ __forceinline__ float silu_f32(float a) { return a / (1.0f + __expf(-a)); }
+__device__ __forceinline__ float activate(float a, int act) {
+  if (act == kActRelu) return fmaxf(a, 0.0f);
+  if (act == kActSilu) return silu_f32(a);
+  if (act == kActGelu) {
+    // 0.5 a (1 + tanh u) = a / (1 + exp(-2u)), u = sqrt(2/pi) (a + 0.044715 a^3)
+    const float u = 1.5957691216057308f * a * fmaf(0.044715f * a, a, 1.0f);
+    return a / (1.0f + __expf(-u));
+  }
+  return a;
+}
+
+// Four consecutive columns n .. n+3 of token row t of the product: v (and, with SwiGLU, the up
+// columns u), the sums without bias.  Adds the bias, applies the activation, adds the residual and
+// stores, rounding once.  Columns at and beyond n_out are left out.
+template <bool GATED>
+__device__ __forceinline__ void epilogue4(const LinearArgs& a, int64_t t, int n, const float (&v)[4],
+                                          const float (&u)[4]) {
+  float r[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int c = min(n + i, a.n_out - 1);
+    const float g = a.bias ? v[i] + a.bias[c] : v[i];
+    if (GATED)
+      r[i] = silu_f32(g) * (a.bias ? u[i] + a.bias[a.n_out + c] : u[i]);
+    else
+      r[i] = activate(g, a.act);
+  }
+  const int64_t at = t * a.n_out + n;
+  if (a.vec && n + 4 <= a.n_out) {
+    if (a.residual) {
+      if (a.res_f32) {
+        const float4 q = *reinterpret_cast<const float4*>(reinterpret_cast<const float*>(a.residual) + at);
+        r[0] += q.x, r[1] += q.y, r[2] += q.z, r[3] += q.w;
+      } else {
+        const uint2 q = *reinterpret_cast<const uint2*>(reinterpret_cast<const uint16_t*>(a.residual) + at);
+        r[0] += bf16_to_f32(q.x & 0xFFFFu), r[1] += __uint_as_float(q.x & 0xFFFF0000u);
+        r[2] += bf16_to_f32(q.y & 0xFFFFu), r[3] += __uint_as_float(q.y & 0xFFFF0000u);
+      }
+    }
+    if (a.out_f32)
+      *reinterpret_cast<float4*>(reinterpret_cast<float*>(a.out) + at) = make_float4(r[0], r[1], r[2], r[3]);
+    else
+      *reinterpret_cast<uint2*>(reinterpret_cast<uint16_t*>(a.out) + at) =
+          make_uint2(f32x2_to_bf16x2_rne(r[0], r[1]), f32x2_to_bf16x2_rne(r[2], r[3]));
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if (n + i >= a.n_out) break;
+    if (a.residual)
+      r[i] += a.res_f32 ? reinterpret_cast<const float*>(a.residual)[at + i]
+                        : bf16_to_f32(reinterpret_cast<const uint16_t*>(a.residual)[at + i]);
+    if (a.out_f32)
+      reinterpret_cast<float*>(a.out)[at + i] = r[i];
+    else
+      reinterpret_cast<uint16_t*>(a.out)[at + i] = (uint16_t)f32_to_bf16_rne(r[i]);
+  }
+}
+
+}  // namespace bitmoe

@@ -364,6 +364,80 @@ moe_status moe_tier_load(const moe_weights* host_w, const moe_weights* slot_w, c
 moe_status moe_tier_remap(const int32_t* topk_ids, int64_t R, const int32_t* slot_of_expert,
                           int32_t* slot_ids, void* stream);
 
+/* ---------------------------------------------------------------- around the expert FFN
+ * The steps of a MoE block directly before and beside the four calls, as one inference step uses
+ * them:  moe_add_rmsnorm (x of the block)  ->  moe_linear (router logits)  ->  moe_route_scored
+ * ->  moe_permute, moe_expert_ffn, moe_combine  ->  moe_linear twice (a shared expert: FC1 with
+ * SwiGLU, FC2 with the routed output as its residual).  They need no workspace, keep no state and
+ * follow the conventions above: one stream, no allocation, no synchronisation, capturable.
+ * The pages describe none of the three; they are the usual definitions, stated in full below.
+ * Arrays do not overlap unless a call says so. */
+typedef enum { MOE_DT_F32 = 1, MOE_DT_BF16 = 2, MOE_DT_MXFP8 = 3 } moe_dtype;
+
+/* moe_add_rmsnorm -- the residual addition and RMS norm of T rows of H values:
+ *     s = x + residual, an fp32 sum rounded to the residual's type (s = x without a residual)
+ *     y = s * weight / sqrt(mean(s^2) + eps)
+ *   x             [T][H], MOE_DT_F32 or MOE_DT_BF16 (x_dtype): both outputs of moe_combine fit
+ *   residual      [T][H] of residual_dtype (F32 or BF16), or NULL
+ *   weight        bf16 [H]
+ *   residual_out  s, in residual_dtype; may be NULL, or residual itself (in place); NULL without a
+ *                 residual
+ *   y             bf16 [T][H], or NULL
+ *   q, q_scales   MXFP8 of the bf16 y (u8 [T][H] e4m3fn elements, u8 [T][H/32] e8m0 scales), bit
+ *                 for bit what moe_mxfp8_quantize makes of y; or both NULL.  y or q is required.
+ * The sum of squares and the scaling are fp32, rounded once to bf16; the norm is taken of s as
+ * rounded, so the call equals an addition followed by a norm of residual_out bit for bit.  A row's
+ * result does not depend on the others.  The sum of squares of a row must stay below the fp32 range.
+ * Errors: INVALID_ARG (bad sizes, types or pointers; eps not a normal positive number; q with
+ * H % 32 != 0; x, residual, residual_out, weight, y not 16-byte aligned, q not 8-byte aligned),
+ * UNSUPPORTED (H % 8 != 0 or H > 16384). */
+moe_status moe_add_rmsnorm(const void* x, int32_t x_dtype, const void* residual, int32_t residual_dtype,
+                           const uint16_t* weight, float eps, int32_t T, int32_t H, void* residual_out,
+                           uint16_t* y, uint8_t* q, uint8_t* q_scales, void* stream);
+
+/* moe_linear -- a dense product with its epilogue, out = act(x W^T + bias) + residual:
+ *   dtype          MOE_DT_BF16:  x bf16 [T][K], w bf16 [N][K]; x_scales, w_scales NULL
+ *                  MOE_DT_MXFP8: x u8 [T][K] e4m3fn with x_scales u8 [T][K/32] e8m0 (as
+ *                  moe_mxfp8_quantize and moe_add_rmsnorm write them), w and w_scales likewise
+ *   bias           f32 [N], or NULL
+ *   act            moe_act.  MOE_ACT_SWIGLU: the first N/2 rows of w (and of bias) are the gate, the
+ *                  others the up projection (the layout of an expert's W1), and
+ *                  out = silu(gate) * up has N/2 columns; the others have N
+ *   residual       [T][columns of out] of residual_dtype (F32 or BF16), or NULL
+ *   out            of out_dtype (F32 or BF16); may be residual itself if the types are equal
+ * Sums are fp32 on the matrix cores; bias, activation and residual are applied in fp32 and the
+ * result is rounded once.  MXFP8 products go to bf16 only: the FP8 matrix cores' sums carry an
+ * error of a few 1e-4 of their rms (measured), which an fp32 output would not show.  The order of a
+ * row's sums may follow T, so its bits may change with the batch size.
+ * Errors: INVALID_ARG (bad sizes, types or pointers; K % 32 != 0 with MXFP8; N odd with SwiGLU; x or
+ * w not 16-byte aligned), UNSUPPORTED (K % 8 != 0; N or K > 2^20; MXFP8 with an F32 output). */
+typedef enum { MOE_ACT_NONE = 0, MOE_ACT_RELU = 1, MOE_ACT_GELU = 2 /* tanh form */, MOE_ACT_SILU = 3,
+               MOE_ACT_SWIGLU = 4 } moe_act;
+moe_status moe_linear(const void* x, const uint8_t* x_scales, const void* w, const uint8_t* w_scales,
+                      int32_t dtype, int32_t T, int32_t N, int32_t K, const float* bias, int32_t act,
+                      const void* residual, int32_t residual_dtype, void* out, int32_t out_dtype, void* stream);
+
+/* moe_route_scored -- moe_route with scores over all experts, a bias for balance and groups:
+ *     p = softmax(logits) over the E experts, or sigmoid(logits)  (score)
+ *     c = p + bias                                                (bias f32[E], or NULL)
+ *     a group's score = the sum of its group_top (1 or 2) largest c; the groups are n_group runs of
+ *     E / n_group consecutive experts, and the topk_group best ones stay
+ *     topk_ids = the k experts of those groups with the largest c, in descending order
+ *     topk_w   = p of the chosen / their sum * scale if renormalize, else p * scale
+ * Ties go to the lower group and to the lower expert.  The choice is that of exact arithmetic to
+ * within 64-bit rounding; without a bias it follows the logits themselves (the same order).
+ * An expert whose c is -inf or NaN (a bias of -inf takes it out of service; a NaN logit) is
+ * chosen only when no other is left, with gate 0, and counts nothing for its group; gates whose
+ * sum is 0 are 0.  All ids lie in [0, E) whatever the logits are.
+ * n_group = 1 (with topk_group = 1) is routing without groups.
+ * Errors: INVALID_ARG as moe_route; a score or group_top that is neither; E % n_group != 0;
+ * topk_group outside [1, n_group]; k > topk_group * E / n_group; scale not finite.  UNSUPPORTED:
+ * n_group > 64. */
+typedef enum { MOE_SCORE_SOFTMAX = 1, MOE_SCORE_SIGMOID = 2 } moe_score;
+moe_status moe_route_scored(const float* logits, const float* bias, int32_t T, int32_t E, int32_t k,
+                            int32_t score, int32_t n_group, int32_t topk_group, int32_t group_top,
+                            int32_t renormalize, float scale, int32_t* topk_ids, float* topk_w, void* stream);
+
 /* moe_debug_dequant -- decode one low-bit expert matrix with the same device code the FFN
  * kernels use, into f32[rows][K] (W1: rows = 2I, K = H; W2: rows = H, K = I), in natural K
  * order.  For tests: the decoded weights must equal the format definition bit for bit.

@@ -29,4 +29,4 @@ Readings taken where the pages are silent or ambiguous are stated next to the co
 that takes them.  Every function here is pinned by tests in ``tests/test_oracle_*.py``
 against worked examples, brute force, closed forms or invariants.
 """
-from . import formats, moe, quant  # noqa: F401
+from . import block, formats, moe, quant  # noqa: F401
