@@ -23,6 +23,10 @@ __device__ __forceinline__ f32x16_t mfma_mxfp8_32x32x64(u32x4 a0, u32x4 a1, u32x
   return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a, b, c, 0, 0, 0, (int)sa, 0, (int)sb);
 }
 
+// The MFMA builtins are pure: an empty volatile asm that reads their results keeps them from sinking
+// past the reads and barriers that follow.
+__device__ __forceinline__ void hold(const f32x16_t& v) { asm volatile("" ::"v"(v)); }
+
 // The activations in fp32 (each a few ulp).  exp overflows to inf for very negative arguments,
 // where the quotient is the right limit 0.
 __device__ __forceinline__ float silu_f32(float a) { return a / (1.0f + __expf(-a)); }
