@@ -53,6 +53,8 @@ struct LinearArgs {
   int res_f32, out_f32;
   int vec;  // rows of out and residual allow 4-column vector accesses
 };
+// few token rows (linear_rows.hip)
+hipError_t launch_linear_rows(const LinearArgs& a, bool mxfp8, hipStream_t s);
 hipError_t launch_linear(const LinearArgs& a, bool mxfp8, hipStream_t s);
 
 }  // namespace bitmoe

@@ -23,15 +23,6 @@ namespace bitmoe {
 namespace {
 
 constexpr int kXcds = 8;
-typedef __attribute__((address_space(3))) void lds_void;
-
-// s_waitcnt vmcnt(N) (and lgkmcnt(0) if LGKM), the other counters not waited on
-template <int N, bool LGKM>
-__device__ __forceinline__ void wait_vm() {
-  static_assert(N >= 0 && N < 64, "vmcnt is 6 bits");
-  __builtin_amdgcn_s_waitcnt((N & 15) | 0x70 | (LGKM ? 0 : 0xF00) | ((N >> 4) << 14));
-}
-
 template <bool MX, bool GATED, int BM, int BN, int WM, int WN, int S, int OCC>
 __global__ __launch_bounds__(64 * WM * WN, OCC) void linear_tile_kernel(LinearArgs a, int m_tiles, int n_tiles) {
   constexpr int NW = WM * WN, kThreads = 64 * NW;
@@ -292,65 +283,6 @@ hipError_t go_tile(const LinearArgs& a, hipStream_t s) {
   return hipGetLastError();
 }
 
-// One wave computes a 32 x 32 tile of the output (two weight tiles with SwiGLU: the gate rows and
-// the up rows of the same columns) straight from global memory.
-template <bool MX, bool GATED>
-__global__ __launch_bounds__(256) void linear_wave_kernel(LinearArgs a, int n_tiles, int64_t tiles) {
-  constexpr int kEs = MX ? 1 : 2;          // bytes of an element
-  constexpr int kStep = MX ? 64 : 16;      // k of one MFMA
-  const int lane = wave_lane(), r32 = lane & 31, hl = lane >> 5;
-  const int64_t tile = (int64_t)blockIdx.x * 4 + threadIdx.x / kWave;
-  if (tile >= tiles) return;
-  const int64_t t0 = tile / n_tiles * 32;
-  const int n0 = (int)(tile % n_tiles) * 32;
-  const int64_t xt = min(t0 + r32, (int64_t)a.T - 1);
-  const int wn = min(n0 + r32, a.n_out - 1);
-  const uint8_t* xr = a.x + xt * a.K * kEs;
-  const uint8_t* wr[2] = {a.w + (int64_t)wn * a.K * kEs, a.w + (int64_t)(GATED ? a.n_out + wn : wn) * a.K * kEs};
-  f32x16_t acc[2];
-#pragma unroll
-  for (int g = 0; g < 2; ++g)
-#pragma unroll
-    for (int i = 0; i < 16; ++i) acc[g][i] = 0.f;
-  const u32x4 zero = {0, 0, 0, 0};
-  auto load = [&](const uint8_t* p, int k) { return k < a.K ? *reinterpret_cast<const u32x4*>(p + (int64_t)k * kEs) : zero; };
-  for (int k0 = 0; k0 < a.K; k0 += kStep) {
-    if constexpr (MX) {
-      const int kb = k0 / 32 + hl, ks = a.K / 32;
-      const u32x4 b0 = load(xr, k0 + 16 * hl), b1 = load(xr, k0 + 32 + 16 * hl);
-      const uint32_t sb = kb < ks ? a.x_scales[xt * ks + kb] : 0;
-#pragma unroll
-      for (int g = 0; g < (GATED ? 2 : 1); ++g) {
-        const uint32_t sa = kb < ks ? a.w_scales[(int64_t)(g ? a.n_out + wn : wn) * ks + kb] : 0;
-        acc[g] = mfma_mxfp8_32x32x64(load(wr[g], k0 + 16 * hl), load(wr[g], k0 + 32 + 16 * hl), b0, b1, acc[g], sa, sb);
-      }
-    } else {
-      const u32x4 b = load(xr, k0 + 8 * hl);
-#pragma unroll
-      for (int g = 0; g < (GATED ? 2 : 1); ++g) acc[g] = mfma_bf16_32x32x16(load(wr[g], k0 + 8 * hl), b, acc[g]);
-    }
-  }
-  const int64_t t = t0 + r32;
-  if (t >= a.T) return;
-#pragma unroll
-  for (int q = 0; q < 4; ++q) {
-    const int n = n0 + 8 * q + 4 * hl;
-    if (n >= a.n_out) continue;
-    float v[4], u[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = acc[0][4 * q + i], u[i] = acc[1][4 * q + i];
-    epilogue4<GATED>(a, t, n, v, u);
-  }
-}
-
-template <bool MX, bool GATED>
-hipError_t go_wave(const LinearArgs& a, hipStream_t s) {
-  const int n_tiles = (a.n_out + 31) / 32;
-  const int64_t tiles = ((int64_t)a.T + 31) / 32 * n_tiles;
-  linear_wave_kernel<MX, GATED><<<(unsigned)((tiles + 3) / 4), 256, 0, s>>>(a, n_tiles, tiles);
-  return hipGetLastError();
-}
-
 template <bool MX, bool GATED>
 hipError_t launch(const LinearArgs& a, hipStream_t s) {
   auto tiles = [&](int bm, int bn) { return (((int64_t)a.T + bm - 1) / bm) * ((a.N + bn - 1) / bn); };
@@ -360,8 +292,8 @@ hipError_t launch(const LinearArgs& a, hipStream_t s) {
     if (tiles(256, 256) >= 128) return go_tile<MX, GATED, 256, 256, 2, 4, 2, 2>(a, s);
   }
   if (tiles(128, 128) >= 192) return go_tile<MX, GATED, 128, 128, 2, 2, 2, 2>(a, s);
-  if (tiles(64, 64) >= 64) return go_tile<MX, GATED, 64, 64, 2, 2, 4, 2>(a, s);
-  return go_wave<MX, GATED>(a, s);
+  if (a.T > 64 && tiles(64, 64) >= 64) return go_tile<MX, GATED, 64, 64, 2, 2, 4, 2>(a, s);
+  return launch_linear_rows(a, MX, s);
 }
 
 }  // namespace

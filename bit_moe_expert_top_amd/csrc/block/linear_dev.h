@@ -23,6 +23,15 @@ __device__ __forceinline__ f32x16_t mfma_mxfp8_32x32x64(u32x4 a0, u32x4 a1, u32x
   return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a, b, c, 0, 0, 0, (int)sa, 0, (int)sb);
 }
 
+typedef __attribute__((address_space(3))) void lds_void;
+
+// s_waitcnt vmcnt(N) (and lgkmcnt(0) if LGKM), the other counters not waited on
+template <int N, bool LGKM>
+__device__ __forceinline__ void wait_vm() {
+  static_assert(N >= 0 && N < 64, "vmcnt is 6 bits");
+  __builtin_amdgcn_s_waitcnt((N & 15) | 0x70 | (LGKM ? 0 : 0xF00) | ((N >> 4) << 14));
+}
+
 // The MFMA builtins are pure: an empty volatile asm that reads their results keeps them from sinking
 // past the reads and barriers that follow.
 __device__ __forceinline__ void hold(const f32x16_t& v) { asm volatile("" ::"v"(v)); }
