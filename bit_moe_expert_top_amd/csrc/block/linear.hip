@@ -23,22 +23,25 @@ namespace bitmoe {
 namespace {
 
 constexpr int kXcds = 8;
-template <bool MX, bool GATED, int BM, int BN, int WM, int WN, int S, int OCC>
+template <bool MX, bool GATED, int BM, int BN, int WM, int WN, int S, int OCC, int kRow, int kSpread>
 __global__ __launch_bounds__(64 * WM * WN, OCC) void linear_tile_kernel(LinearArgs a, int m_tiles, int n_tiles) {
   constexpr int NW = WM * WN, kThreads = 64 * NW;
   constexpr int AT = BM / WM / 32, BT = BN / WN / 32;   // token and weight MFMA tiles of a wave
-  constexpr int kEs = MX ? 1 : 2, kRow = 128, kStepK = kRow / kEs;
-  constexpr int kSub = MX ? 2 : 4;                      // MFMA sub-steps of a step
+  constexpr int kEs = MX ? 1 : 2, kStepK = kRow / kEs;
   constexpr int kCh = MX ? 2 : 1;                       // 16-byte chunks of a lane per operand and sub-step
-  constexpr int UA = BM / (8 * NW), UB = BN / (8 * NW);
+  constexpr int kSub = kRow / (32 * kCh);               // MFMA sub-steps of a step
+  constexpr int kRows = 1024 / kRow, kChunks = kRow / 16;  // rows of a load, chunks of a row
+  constexpr int UA = BM / (kRows * NW), UB = BN / (kRows * NW);
   constexpr int LD = UA + UB;  // direct loads per wave and stage (the waits below count at least these)
-  constexpr int kStage = (BM + BN) * kRow, kScale = MX ? (BM + BN) * 4 : 16;
-  static_assert(S == 2 || S == 4, "ring depth");
-  static_assert(BM % (8 * NW) == 0 && BN % (8 * NW) == 0 && NW % 4 == 0 && (!MX || BM + BN <= kThreads), "loads");
+  constexpr int kStage = (BM + BN) * kRow, kScale = MX ? BM + BN : 4;
+  static_assert(LD % (kSpread * AT) == 0 || kSpread == 1, "refill parts");
+  static_assert(S >= 2 && S <= 5 && (kRow == 128 || (kRow == 64 && !MX)), "ring");
+  static_assert(BM % (kRows * NW) == 0 && BN % (kRows * NW) == 0 && NW % 4 == 0 , "loads");
   // one object per stage: the compiler tracks direct loads per object, so a read of one stage does
   // not wait for another's
-  __shared__ __align__(16) uint8_t st0[kStage], st1[kStage], st2[S > 2 ? kStage : 16], st3[S > 2 ? kStage : 16];
-  __shared__ uint32_t sc0[kScale / 4], sc1[kScale / 4], sc2[S > 2 ? kScale / 4 : 4], sc3[S > 2 ? kScale / 4 : 4];
+  __shared__ __align__(16) uint8_t st0[kStage], st1[kStage], st2[S > 2 ? kStage : 16], st3[S > 3 ? kStage : 16],
+      st4[S > 4 ? kStage : 16];
+  __shared__ uint32_t sc0[kScale], sc1[kScale], sc2[S > 2 ? kScale : 4], sc3[S > 3 ? kScale : 4], sc4[S > 4 ? kScale : 4];
   const int tid = threadIdx.x, lane = wave_lane();
   const int w = __builtin_amdgcn_readfirstlane(tid / kWave);
   const int wm = w % WM, wn = w / WM, r32 = lane & 31, hl = lane >> 5;
@@ -63,106 +66,104 @@ __global__ __launch_bounds__(64 * WM * WN, OCC) void linear_tile_kernel(LinearAr
   // global addresses: a resource per operand that spans the tile's rows, a byte offset per lane and
   // 8-row load; rows past the end have an offset past the resource and read zeros
   const int rows_x = (int)min((int64_t)BM, a.T - t0), rows_w = min(GATED ? BN / 2 : BN, a.n_out - n0);
-  const bool up = GATED && ((w >> 1) & 1);  // this wave's loads fetch up rows
+  const bool up = GATED && ((w * kRows >> 4) & 1);  // this wave's loads fetch up rows
   const buf_rsrc rx = make_rsrc(a.x + t0 * kb_bytes, (uint32_t)rows_x * kb_bytes);
   const int64_t w_first = (up ? a.n_out : 0) + (int64_t)n0;
   const buf_rsrc rw = make_rsrc(a.w + w_first * kb_bytes, (uint32_t)rows_w * kb_bytes);
-  const int prow = lane >> 3;
-  const uint32_t chunk = 16u * (uint32_t)((lane & 7) ^ ((4 * w + (prow >> 1)) & 7));
+  const int prow = lane / kChunks;
+  auto swizzle = [](int row) { return kRow == 128 ? row >> 1 & 7 : row >> 2 & 3; };
+  const uint32_t chunk = 16u * (uint32_t)(lane % kChunks ^ swizzle(kRows * w + prow));
   uint32_t xoff[UA], woff[UB];
 #pragma unroll
   for (int u = 0; u < UA; ++u) {
-    const int r = 8 * (NW * u + w) + prow;
+    const int r = kRows * (NW * u + w) + prow;
     xoff[u] = r < rows_x ? (uint32_t)r * kb_bytes + chunk : kOffNone;
   }
   // LDS weight row j -> weight row of the tile (among the gate or up rows with SwiGLU)
   auto wrow = [&](int j) { return GATED ? 16 * (j >> 5) + (j & 15) : j; };
 #pragma unroll
   for (int u = 0; u < UB; ++u) {
-    const int r = wrow(8 * (NW * u + w) + prow);
+    const int r = wrow(kRows * (NW * u + w) + prow);
     woff[u] = r < rows_w ? (uint32_t)r * kb_bytes + chunk : kOffNone;
   }
-  // MXFP8: thread j < BM + BN fetches the four scales of stage row j
-  const uint8_t* scale_row = nullptr;
-  if (MX && tid < BM + BN) {
+  // MXFP8: thread j fetches the four scales of stage rows j, j + kThreads, ...
+  constexpr int SR = MX ? (BM + BN + kThreads - 1) / kThreads : 1;
+  const uint8_t* scale_row[SR];
+  if (MX) {
     const int ks = K / 32;
-    if (tid < BM) {
-      if (tid < rows_x) scale_row = a.x_scales + (t0 + tid) * ks;
-    } else {
-      const int j = tid - BM, r = wrow(j);
-      if (r < rows_w) scale_row = a.w_scales + ((GATED && (j & 16) ? a.n_out : 0) + (int64_t)n0 + r) * ks;
+#pragma unroll
+    for (int c = 0; c < SR; ++c) {
+      const int j = tid + c * kThreads, r = wrow(j - BM);
+      scale_row[c] = nullptr;
+      if (j < BM) {
+        if (j < rows_x) scale_row[c] = a.x_scales + (t0 + j) * ks;
+      } else if (j < BM + BN && r < rows_w) {
+        scale_row[c] = a.w_scales + ((GATED && ((j - BM) & 16) ? a.n_out : 0) + (int64_t)n0 + r) * ks;
+      }
     }
   }
-  uint32_t sreg[S];
+  uint32_t sreg[S][SR];
 
   // the stage buffers by index (a constant wherever they are used)
-  auto stage = [&](int d) -> uint8_t* { return d == 0 ? st0 : d == 1 ? st1 : d == 2 ? st2 : st3; };
-  auto scales = [&](int d) -> uint32_t* { return d == 0 ? sc0 : d == 1 ? sc1 : d == 2 ? sc2 : sc3; };
-  auto load = [&](int d, int kb) {
-    uint8_t* st = stage(d);
-    const int ko = kb * kRow;
-    if (MX) {
+  auto stage = [&](int d) -> uint8_t* { return d == 0 ? st0 : d == 1 ? st1 : d == 2 ? st2 : d == 3 ? st3 : st4; };
+  auto scales = [&](int d) -> uint32_t* { return d == 0 ? sc0 : d == 1 ? sc1 : d == 2 ? sc2 : d == 3 ? sc3 : sc4; };
+  // The scales of stage kb (into a register) and direct load i of UA + UB (the token rows, then the
+  // weight rows) into buffer d.  inner: not the last stage.
+  auto load_scales = [&](int d, int kb, bool inner) {
+    if (!MX) return;
+#pragma unroll
+    for (int c = 0; c < SR; ++c) {
       uint32_t v = 0;
-      if (scale_row) {
-        const int left = K / 32 - 4 * kb;
-        const uint8_t* p = scale_row + 4 * kb;
+      if (scale_row[c]) {
+        const int left = inner ? 4 : K / 32 - 4 * kb;
+        const uint8_t* p = scale_row[c] + 4 * kb;
         if (left >= 4) {
           __builtin_memcpy(&v, p, 4);
         } else {
           for (int i = 0; i < left; ++i) v |= (uint32_t)p[i] << (8 * i);
         }
       }
-      sreg[d] = v;
+      sreg[d][c] = v;
     }
-    if (tail && kb == nk - 1) {
-      const bool in = ko + (int)chunk < kb_bytes;  // a chunk is all inside the row or all outside
+  };
+  auto load_one = [&](int d, int kb, int i, bool in) {
+    const bool is_x = i < UA;
+    uint8_t* dst = stage(d) + (is_x ? 1024 * (NW * i + w) : BM * kRow + 1024 * (NW * (i - UA) + w));
+    const uint32_t off = is_x ? xoff[is_x ? i : 0] : woff[is_x ? 0 : i - UA];
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(is_x ? rx : rw, (lds_void*)dst, 16, (int)(in ? off : kOffNone), kb * kRow,
+                                             0, 0);
+  };
+  // the first n direct loads of a stage
+  auto load = [&](int d, int kb, bool inner, int n) {
+    load_scales(d, kb, inner);
+    // a chunk is all inside its row or all outside
+    const bool in = inner || !tail || kb < nk - 1 || kb * kRow + (int)chunk < kb_bytes;
 #pragma unroll
-      for (int u = 0; u < UA; ++u)
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(rx, (lds_void*)(st + 1024 * (NW * u + w)), 16,
-                                                 (int)(in ? xoff[u] : kOffNone), ko, 0, 0);
-#pragma unroll
-      for (int u = 0; u < UB; ++u)
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(rw, (lds_void*)(st + BM * kRow + 1024 * (NW * u + w)), 16,
-                                                 (int)(in ? woff[u] : kOffNone), ko, 0, 0);
-      return;
-    }
-#pragma unroll
-    for (int u = 0; u < UA; ++u)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(rx, (lds_void*)(st + 1024 * (NW * u + w)), 16, (int)xoff[u], ko, 0, 0);
-#pragma unroll
-    for (int u = 0; u < UB; ++u)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(rw, (lds_void*)(st + BM * kRow + 1024 * (NW * u + w)), 16, (int)woff[u],
-                                               ko, 0, 0);
+    for (int i = 0; i < LD; ++i)
+      if (i < n) load_one(d, kb, i, in);
   };
 
-  // a lane's chunk offsets: rows 32 t + r32 share (row / 2) % 8, so the swizzle is the same for
-  // every tile.  Sub-step j: bf16 chunk 2 j + hl; MXFP8 chunks 4 j + hl and 4 j + 2 + hl.
-  uint32_t cofs[4];
+  // a lane's chunk offsets: the swizzle has a period of 16 rows, so it is the same for every tile.  Sub-step j: bf16 chunk 2 j + hl; MXFP8 chunks 4 j + hl and 4 j + 2 + hl.
+  uint32_t cofs[kChunks / 2];
 #pragma unroll
-  for (int j = 0; j < 4; ++j) cofs[j] = 16u * (uint32_t)((2 * j + hl) ^ ((r32 >> 1) & 7));
+  for (int j = 0; j < kChunks / 2; ++j) cofs[j] = 16u * (uint32_t)((2 * j + hl) ^ swizzle(r32));
   const uint32_t xbase = (uint32_t)(32 * AT * wm + r32) * kRow, wbase = (uint32_t)(BM + 32 * BT * wn + r32) * kRow;
   struct Ops {
     u32x4 x[AT][kCh], w[BT][kCh];
     uint32_t sx[AT], sw[BT];
   };
-  auto read = [&](Ops& o, int d, int j) {
-    const uint8_t* st = stage(d);
+  // the operands of sub-step j of buffer d: weight tile b, token tile t
+  auto read_w = [&](Ops& o, int d, int j, int b) {
 #pragma unroll
-    for (int c = 0; c < kCh; ++c) {
+    for (int c = 0; c < kCh; ++c)
+      o.w[b][c] = *reinterpret_cast<const u32x4*>(stage(d) + wbase + cofs[kCh * j + c] + 32 * kRow * b);
+    if (MX) o.sw[b] = reinterpret_cast<const uint8_t*>(scales(d) + BM + 32 * (BT * wn + b) + r32)[2 * j + hl];
+  };
+  auto read_x = [&](Ops& o, int d, int j, int t) {
 #pragma unroll
-      for (int t = 0; t < BT; ++t)
-        o.w[t][c] = *reinterpret_cast<const u32x4*>(st + wbase + cofs[kCh * j + c] + 32 * kRow * t);
-#pragma unroll
-      for (int t = 0; t < AT; ++t)
-        o.x[t][c] = *reinterpret_cast<const u32x4*>(st + xbase + cofs[kCh * j + c] + 32 * kRow * t);
-    }
-    if (MX) {
-      const uint8_t* sc = reinterpret_cast<const uint8_t*>(scales(d)) + 2 * j + hl;
-#pragma unroll
-      for (int t = 0; t < BT; ++t) o.sw[t] = sc[4 * (BM + 32 * (BT * wn + t) + r32)];
-#pragma unroll
-      for (int t = 0; t < AT; ++t) o.sx[t] = sc[4 * (32 * (AT * wm + t) + r32)];
-    }
+    for (int c = 0; c < kCh; ++c)
+      o.x[t][c] = *reinterpret_cast<const u32x4*>(stage(d) + xbase + cofs[kCh * j + c] + 32 * kRow * t);
+    if (MX) o.sx[t] = reinterpret_cast<const uint8_t*>(scales(d) + 32 * (AT * wm + t) + r32)[2 * j + hl];
   };
   f32x16_t acc[AT][BT];
 #pragma unroll
@@ -171,114 +172,187 @@ __global__ __launch_bounds__(64 * WM * WN, OCC) void linear_tile_kernel(LinearAr
     for (int b = 0; b < BT; ++b)
 #pragma unroll
       for (int i = 0; i < 16; ++i) acc[t][b][i] = 0.f;
-  auto mfma = [&](const Ops& o) {
+  // the MFMAs of token tile t
+  auto mfma = [&](const Ops& o, int t) {
 #pragma unroll
-    for (int t = 0; t < AT; ++t)
+    for (int b = 0; b < BT; ++b) {
+      if constexpr (MX)
+        acc[t][b] = mfma_mxfp8_32x32x64(o.w[b][0], o.w[b][1], o.x[t][0], o.x[t][1], acc[t][b], o.sw[b], o.sx[t]);
+      else
+        acc[t][b] = mfma_bf16_32x32x16(o.w[b][0], o.x[t][0], acc[t][b]);
+    }
 #pragma unroll
-      for (int b = 0; b < BT; ++b) {
-        if constexpr (MX)
-          acc[t][b] = mfma_mxfp8_32x32x64(o.w[b][0], o.w[b][1], o.x[t][0], o.x[t][1], acc[t][b], o.sw[b], o.sx[t]);
-        else
-          acc[t][b] = mfma_bf16_32x32x16(o.w[b][0], o.x[t][0], acc[t][b]);
-      }
-#pragma unroll
-    for (int t = 0; t < AT; ++t)
-#pragma unroll
-      for (int b = 0; b < BT; ++b) hold(acc[t][b]);
+    for (int b = 0; b < BT; ++b) hold<(AT * BT > 8)>(acc[t][b]);
   };
 
   using I0 = std::integral_constant<int, 0>;
   using I1 = std::integral_constant<int, 1>;
   using I2 = std::integral_constant<int, 2>;
   using I3 = std::integral_constant<int, 3>;
+  using I4 = std::integral_constant<int, 4>;
   auto put_scales = [&](int d) {
-    if (MX && tid < BM + BN) scales(d)[tid] = sreg[d];
-  };
 #pragma unroll
-  for (int d = 0; d < S; ++d)
-    if (d < nk) load(d, d);
-  if (nk >= S)
-    wait_vm<(S - 1) * LD, false>();
-  else
+    for (int c = 0; c < SR; ++c)
+      if (MX && tid + c * kThreads < BM + BN) scales(d)[tid + c * kThreads] = sreg[d][c];
+  };
+  // Stages 0 .. S - 1; of the last one only the first part of kSpread, the others are fetched by step 0.
+  if (nk > S) {
+#pragma unroll
+    for (int d = 0; d < S; ++d) load(d, d, true, d < S - 1 ? LD : LD / kSpread);
+    wait_vm<(S - 2) * LD + LD / kSpread, false>();
+  } else {
+#pragma unroll
+    for (int d = 0; d < S; ++d)
+      if (d < nk) load(d, d, false, d < S - 1 ? LD : LD / kSpread);
     wait_vm<0, false>();
+  }
   put_scales(0);
   wait_vm<63, true>();
   asm volatile("s_barrier" ::: "memory");
   Ops op[2];
-  read(op[0], 0, 0);
-  // step kb, its stage in buffer D and in LDS for all waves, its first operands in op[0]
-  auto step = [&](auto D, int kb) {
-    constexpr int d = decltype(D)::value;
-    constexpr int next = (d + 1) % S;
 #pragma unroll
-    for (int j = 0; j + 1 < kSub; ++j) {
-      read(op[(j + 1) & 1], d, j + 1);
-      __builtin_amdgcn_sched_barrier(0);
-      mfma(op[j & 1]);
-      __builtin_amdgcn_sched_barrier(0);
+  for (int b = 0; b < BT; ++b) read_w(op[0], 0, 0, b);
+#pragma unroll
+  for (int t = 0; t < AT; ++t) read_x(op[0], 0, 0, t);
+  // Step kb, its stage in buffer D and in LDS for all waves, its first operands in op[0].  MAIN: the
+  // stages it fetches exist and are not the last, so this step loads and waits without a branch.  (Branches
+  // around loads and waits let the compiler think at the loop's head that a buffer may still be
+  // filling, and wait there for every load in flight.)
+  auto step = [&](auto D, auto MAIN_, int kb) {
+    constexpr int d = decltype(D)::value, next = (d + 1) % S;
+    constexpr bool kMain = decltype(MAIN_)::value;
+    // Sub-step j: per token tile, the reads of a share of the next sub-step's operands, then the MFMAs.
+    // In the last sub-step those are the next stage's, behind the barrier, and the direct loads that
+    // refill this buffer are issued between the MFMAs too.
+#pragma unroll
+    for (int j = 0; j < kSub; ++j) {
+      const bool last = j == kSub - 1;
+      const bool more = !last || kMain || kb + 1 < nk;
+      // sub-step part p of the refill of a buffer: p = 0 in the last sub-step of the step that read it,
+      // the others in the first sub-steps of the next step
+      const int p = last ? 0 : j + 1, fd = last ? d : (d + S - 1) % S, fk = last ? kb + S : kb - 1 + S;
+      static_assert(kSpread <= kSub, "a refill ends before the next step's barrier");
+      const bool refill = p < kSpread && (kMain || fk < nk);
+      const bool in = kMain || !tail || fk < nk - 1 || fk * kRow + (int)chunk < kb_bytes;
+      if (last && more) {
+        // this wave's loads of the next stage have landed (those of later ones may be in flight)
+        if (kMain || kb + S <= nk)
+          wait_vm<(S - 2) * LD, false>();
+        else
+          wait_vm<0, false>();
+        put_scales(next);
+        wait_vm<63, true>();
+        asm volatile("s_barrier" ::: "memory");
+        if (refill) load_scales(fd, fk, kMain);
+      }
+#pragma unroll
+      for (int t = 0; t < AT; ++t) {
+        if (more) {
+          // three tiles' reads per token tile, the weight tiles first (all MFMAs of a token tile need
+          // them), so that the last ones have landed when the sub-step ends
+#pragma unroll
+          for (int i = 0; i < BT + AT; ++i) {
+            if (i / 3 != t && !(t == AT - 1 && i / 3 > t)) continue;
+            if (i < BT)
+              read_w(op[(j + 1) & 1], last ? next : d, last ? 0 : j + 1, i < BT ? i : 0);
+            else
+              read_x(op[(j + 1) & 1], last ? next : d, last ? 0 : j + 1, i < BT ? 0 : i - BT);
+          }
+        }
+        if (refill) {
+#pragma unroll
+          for (int i = 0; i < LD; ++i)
+            if (i * AT * kSpread / LD == p * AT + t) load_one(fd, fk, i, in);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+        mfma(op[j & 1], t);
+        __builtin_amdgcn_sched_barrier(0);
+      }
     }
-    if (kb + 1 < nk) {
-      // this wave's loads of the next stage have landed (those of later ones may be in flight)
-      if (S > 2 && kb + S <= nk)
-        wait_vm<(S - 2) * LD, false>();
-      else
-        wait_vm<0, false>();
-      put_scales(next);
-      wait_vm<63, true>();
-      asm volatile("s_barrier" ::: "memory");
-      if (kb + S < nk) load(d, kb + S);
-      read(op[0], next, 0);
-      __builtin_amdgcn_sched_barrier(0);
-    }
-    mfma(op[(kSub - 1) & 1]);
-    __builtin_amdgcn_sched_barrier(0);
   };
-  for (int kb = 0; kb < nk; kb += S) {
-    step(I0{}, kb);
-    if (kb + 1 < nk) step(I1{}, kb + 1);
-    if constexpr (S > 2) {
-      if (kb + 2 < nk) step(I2{}, kb + 2);
-      if (kb + 3 < nk) step(I3{}, kb + 3);
-    }
+  int kb = 0;
+  for (; kb + 2 * S < nk; kb += S) {
+    step(I0{}, std::true_type{}, kb);
+    step(I1{}, std::true_type{}, kb + 1);
+    if constexpr (S > 2) step(I2{}, std::true_type{}, kb + 2);
+    if constexpr (S > 3) step(I3{}, std::true_type{}, kb + 3);
+    if constexpr (S > 4) step(I4{}, std::true_type{}, kb + 4);
+  }
+  // at most 2 S steps are left
+#pragma unroll
+  for (int i = 0; i < 2; ++i, kb += S) {
+    if (kb < nk) step(I0{}, std::false_type{}, kb);
+    if (kb + 1 < nk) step(I1{}, std::false_type{}, kb + 1);
+    if constexpr (S > 2)
+      if (kb + 2 < nk) step(I2{}, std::false_type{}, kb + 2);
+    if constexpr (S > 3)
+      if (kb + 3 < nk) step(I3{}, std::false_type{}, kb + 3);
+    if constexpr (S > 4)
+      if (kb + 4 < nk) step(I4{}, std::false_type{}, kb + 4);
   }
 
-  // ---- epilogue: 32 token rows of the wave at a time through the wave's part of the first stage
-  // (rows of 32 BT sums and a pad of four), then four consecutive columns per lane
+  // ---- epilogue: 32 token rows of the wave at a time through the wave's part of the stages (rows of
+  // 32 BT sums and a pad of four), then four consecutive columns per lane.  The residual values of the
+  // next 32 rows are fetched before this turn's stores: out may be the residual, so a load behind a
+  // store would wait for it.
   constexpr int kPitch = 32 * BT + 4, kCols = GATED ? 16 * BT : 32 * BT, kLanes = kCols / 4;
-  static_assert(NW * 32 * kPitch * 4 <= 2 * kStage, "epilogue staging");
-  __syncthreads();
-  constexpr bool kTwo = NW * 32 * kPitch * 4 > kStage;  // half the waves in each of two stages
-  float* ep = reinterpret_cast<float*>(kTwo && w >= NW / 2 ? st1 : st0) + (kTwo ? w % (NW / 2) : w) * 32 * kPitch;
-  const int ec = 4 * (lane % kLanes), n = n0 + kCols * wn + ec;
+  constexpr int kStep = kWave / kLanes, kStores = 32 / kStep;  // rows of a store, stores of a turn
+  const int ec = 4 * (lane % kLanes), n = n0 + kCols * wn + ec, er = lane / kLanes;
+  const int64_t row0 = t0 + 32 * AT * wm + er;  // this lane's first row
+  const int rows = n < a.n_out ? (int)max((int64_t)0, min((int64_t)32 * AT, a.T - (row0 - er))) - er : 0;
+  const int64_t at0 = row0 * a.n_out + n;
+  const FourBias bias = load_bias4<GATED>(a, n);
+  Four res[kStores];
+  auto fetch = [&](int t) {
+    if (a.residual) {
 #pragma unroll
-  for (int t = 0; t < AT; ++t) {
+      for (int i = 0; i < kStores; ++i)
+        if (32 * t + i * kStep < rows) res[i] = load_residual4(a, at0 + (int64_t)(32 * t + i * kStep) * a.n_out, n);
+    }
+  };
+  fetch(0);
+  __syncthreads();
+  constexpr int kFit = kStage / (32 * kPitch * 4);  // waves whose part fits one stage
+  static_assert((NW + kFit - 1) / kFit <= S, "epilogue staging");
+  float* ep = reinterpret_cast<float*>(stage(w / kFit)) + w % kFit * 32 * kPitch;
+  auto put = [&](const f32x16_t(&v)[BT]) {
 #pragma unroll
     for (int b = 0; b < BT; ++b)
 #pragma unroll
       for (int q = 0; q < 4; ++q)
         *reinterpret_cast<float4*>(ep + r32 * kPitch + 32 * b + 8 * q + 4 * hl) =
-            make_float4(acc[t][b][4 * q], acc[t][b][4 * q + 1], acc[t][b][4 * q + 2], acc[t][b][4 * q + 3]);
-    __builtin_amdgcn_wave_barrier();
+            make_float4(v[b][4 * q], v[b][4 * q + 1], v[b][4 * q + 2], v[b][4 * q + 3]);
+  };
+  // with SwiGLU column c of the wave has its gate sum at 32 (c / 16) + c % 16, its up sum 16 further on
+  const float* get = ep + er * kPitch + (GATED ? 32 * (ec / 16) + ec % 16 : ec);
+  // the loop is not unrolled, for the size of its code; the sums are picked with constant indexes
+#pragma unroll 1
+  for (int t = 0; t < AT; ++t) {
 #pragma unroll
-    for (int r0 = 0; r0 < 32; r0 += kWave / kLanes) {
-      const int r = r0 + lane / kLanes;
-      const int64_t tok = t0 + 32 * (AT * wm + t) + r;
-      // with SwiGLU column c of the wave has its gate sum at 32 (c / 16) + c % 16, its up sum 16 further on
-      const float* p = ep + r * kPitch + (GATED ? 32 * (ec / 16) + ec % 16 : ec);
-      const float4 v4 = *reinterpret_cast<const float4*>(p);
-      const float4 u4 = GATED ? *reinterpret_cast<const float4*>(p + 16) : v4;
+    for (int i = 0; i < AT; ++i)
+      if (t == i) put(acc[i]);
+    __builtin_amdgcn_wave_barrier();
+    Four now[kStores];
+#pragma unroll
+    for (int i = 0; i < kStores; ++i) now[i] = res[i];
+    if (t + 1 < AT) fetch(t + 1);
+#pragma unroll
+    for (int i = 0; i < kStores; ++i) {
+      const float4 v4 = *reinterpret_cast<const float4*>(get + i * kStep * kPitch);
+      const float4 u4 = GATED ? *reinterpret_cast<const float4*>(get + i * kStep * kPitch + 16) : v4;
       const float v[4] = {v4.x, v4.y, v4.z, v4.w}, u[4] = {u4.x, u4.y, u4.z, u4.w};
-      if (tok < a.T && n < a.n_out) epilogue4<GATED>(a, tok, n, v, u);
+      if (32 * t + i * kStep < rows)
+        epilogue4<GATED>(a, at0 + (int64_t)(32 * t + i * kStep) * a.n_out, n, v, u, bias, now[i]);
     }
     __builtin_amdgcn_wave_barrier();
   }
 }
 
-template <bool MX, bool GATED, int BM, int BN, int WM, int WN, int S, int OCC>
+template <bool MX, bool GATED, int BM, int BN, int WM, int WN, int S, int OCC, int kRow, int kSpread>
 hipError_t go_tile(const LinearArgs& a, hipStream_t s) {
   const int64_t m_tiles = ((int64_t)a.T + BM - 1) / BM;
   const int bn = GATED ? BN / 2 : BN, n_tiles = (a.n_out + bn - 1) / bn;
-  linear_tile_kernel<MX, GATED, BM, BN, WM, WN, S, OCC>
+  linear_tile_kernel<MX, GATED, BM, BN, WM, WN, S, OCC, kRow, kSpread>
       <<<(unsigned)(m_tiles * n_tiles), 64 * WM * WN, 0, s>>>(a, (int)m_tiles, n_tiles);
   return hipGetLastError();
 }
@@ -287,12 +361,12 @@ template <bool MX, bool GATED>
 hipError_t launch(const LinearArgs& a, hipStream_t s) {
   auto tiles = [&](int bm, int bn) { return (((int64_t)a.T + bm - 1) / bm) * ((a.N + bn - 1) / bn); };
   if constexpr (MX) {
-    if (tiles(256, 128) >= 256) return go_tile<MX, GATED, 256, 128, 4, 2, 2, 2>(a, s);
+    if (tiles(256, 128) >= 256) return go_tile<MX, GATED, 256, 128, 4, 2, 2, 2, 128, 1>(a, s);
   } else {
-    if (tiles(256, 256) >= 128) return go_tile<MX, GATED, 256, 256, 2, 4, 2, 2>(a, s);
+    if (tiles(256, 256) >= 128) return go_tile<MX, GATED, 256, 256, 2, 4, 2, 2, 128, 2>(a, s);
   }
-  if (tiles(128, 128) >= 192) return go_tile<MX, GATED, 128, 128, 2, 2, 2, 2>(a, s);
-  if (a.T > 64 && tiles(64, 64) >= 64) return go_tile<MX, GATED, 64, 64, 2, 2, 4, 2>(a, s);
+  if (tiles(128, 128) >= 192) return go_tile<MX, GATED, 128, 128, 2, 2, 2, 2, 128, 1>(a, s);
+  if (a.T > 64 && tiles(64, 64) >= 64) return go_tile<MX, GATED, 64, 64, 2, 2, 4, 2, 128, 1>(a, s);
   return launch_linear_rows(a, MX, s);
 }
 

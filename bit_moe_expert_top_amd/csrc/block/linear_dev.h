@@ -34,50 +34,110 @@ __device__ __forceinline__ void wait_vm() {
 
 // The MFMA builtins are pure: an empty volatile asm that reads their results keeps them from sinking
 // past the reads and barriers that follow.
-__device__ __forceinline__ void hold(const f32x16_t& v) { asm volatile("" ::"v"(v)); }
-
-// The activations in fp32 (each a few ulp).  exp overflows to inf for very negative arguments,
-// where the quotient is the right limit 0.
-__device__ __forceinline__ float silu_f32(float a) { return a / (1.0f + __expf(-a)); }
-__device__ __forceinline__ float activate(float a, int act) {
-  if (act == kActRelu) return fmaxf(a, 0.0f);
-  if (act == kActSilu) return silu_f32(a);
-  if (act == kActGelu) {
-    // 0.5 a (1 + tanh u) = a / (1 + exp(-2u)), u = sqrt(2/pi) (a + 0.044715 a^3)
-    const float u = 1.5957691216057308f * a * fmaf(0.044715f * a, a, 1.0f);
-    return a / (1.0f + __expf(-u));
-  }
-  return a;
+// ACC: accumulation registers (kernels whose sums leave no room in the others).
+template <bool ACC>
+__device__ __forceinline__ void hold(const f32x16_t& v) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  if constexpr (ACC)
+    asm volatile("" ::"a"(v));
+  else
+    asm volatile("" ::"v"(v));
+#endif
 }
 
-// Four consecutive columns n .. n+3 of token row t of the product: v (and, with SwiGLU, the up
-// columns u), the sums without bias.  Adds the bias, applies the activation, adds the residual and
-// stores, rounding once.  Columns at and beyond n_out are left out.
+// The activations in fp32 (a few ulp each: v_exp_f32 and v_rcp_f32 are good to one).  exp overflows
+// to inf for very negative arguments, whose reciprocal gives the right limit 0.
+__device__ __forceinline__ float silu_f32(float a) { return a * __builtin_amdgcn_rcpf(1.0f + __expf(-a)); }
+template <int N>
+__device__ __forceinline__ void activate(float (&r)[N], int act) {
+  if (act == kActRelu) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) r[i] = fmaxf(r[i], 0.0f);
+  } else if (act == kActSilu) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) r[i] = silu_f32(r[i]);
+  } else if (act == kActGelu) {
+    // 0.5 a (1 + tanh u) = a / (1 + exp(-2u)), u = sqrt(2/pi) (a + 0.044715 a^3)
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const float u = 1.5957691216057308f * r[i] * fmaf(0.044715f * r[i], r[i], 1.0f);
+      r[i] = r[i] * __builtin_amdgcn_rcpf(1.0f + __expf(-u));
+    }
+  }
+}
+
+// The epilogue works on four consecutive columns n .. n + 3 of a token row at a time; columns at and
+// beyond n_out are left out.
+
+// Four residual values as they are stored: 16 bytes of fp32 or 8 of bf16.  at: t * n_out + n.
+struct Four {
+  uint32_t w[4];
+};
+__device__ __forceinline__ Four load_residual4(const LinearArgs& a, int64_t at, int n) {
+  Four r{};
+  if (a.vec) {
+    if (a.res_f32) {
+      const uint4 q = *reinterpret_cast<const uint4*>(reinterpret_cast<const float*>(a.residual) + at);
+      r.w[0] = q.x, r.w[1] = q.y, r.w[2] = q.z, r.w[3] = q.w;
+    } else {
+      const uint2 q = *reinterpret_cast<const uint2*>(reinterpret_cast<const uint16_t*>(a.residual) + at);
+      r.w[0] = q.x, r.w[1] = q.y;
+    }
+    return r;
+  }
+  if (a.res_f32) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (n + i < a.n_out) r.w[i] = reinterpret_cast<const uint32_t*>(a.residual)[at + i];
+  } else {
+    const uint16_t* p = reinterpret_cast<const uint16_t*>(a.residual) + at;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (n + i < a.n_out) r.w[i / 2] |= (uint32_t)p[i] << (16 * (i % 2));
+  }
+  return r;
+}
+
+// The bias of four columns (and of their up rows with SwiGLU), zero without one.
+struct FourBias {
+  float g[4], u[4];
+};
 template <bool GATED>
-__device__ __forceinline__ void epilogue4(const LinearArgs& a, int64_t t, int n, const float (&v)[4],
-                                          const float (&u)[4]) {
-  float r[4];
+__device__ __forceinline__ FourBias load_bias4(const LinearArgs& a, int n) {
+  FourBias b;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const int c = min(n + i, a.n_out - 1);
-    const float g = a.bias ? v[i] + a.bias[c] : v[i];
-    if (GATED)
-      r[i] = silu_f32(g) * (a.bias ? u[i] + a.bias[a.n_out + c] : u[i]);
-    else
-      r[i] = activate(g, a.act);
+    b.g[i] = a.bias ? a.bias[c] : 0.0f;
+    b.u[i] = GATED && a.bias ? a.bias[a.n_out + c] : 0.0f;
   }
-  const int64_t at = t * a.n_out + n;
-  if (a.vec && n + 4 <= a.n_out) {
-    if (a.residual) {
-      if (a.res_f32) {
-        const float4 q = *reinterpret_cast<const float4*>(reinterpret_cast<const float*>(a.residual) + at);
-        r[0] += q.x, r[1] += q.y, r[2] += q.z, r[3] += q.w;
-      } else {
-        const uint2 q = *reinterpret_cast<const uint2*>(reinterpret_cast<const uint16_t*>(a.residual) + at);
-        r[0] += bf16_to_f32(q.x & 0xFFFFu), r[1] += __uint_as_float(q.x & 0xFFFF0000u);
-        r[2] += bf16_to_f32(q.y & 0xFFFFu), r[3] += __uint_as_float(q.y & 0xFFFF0000u);
-      }
+  return b;
+}
+
+// v (and, with SwiGLU, the up columns u): the sums without bias.  Adds the bias, applies the
+// activation, adds the residual and stores, rounding once.
+template <bool GATED>
+__device__ __forceinline__ void epilogue4(const LinearArgs& a, int64_t at, int n, const float (&v)[4],
+                                          const float (&u)[4], const FourBias& bias, const Four& res) {
+  float r[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) r[i] = v[i] + bias.g[i];
+  if constexpr (GATED) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) r[i] = silu_f32(r[i]) * (u[i] + bias.u[i]);
+  } else {
+    activate(r, a.act);
+  }
+  if (a.residual) {
+    if (a.res_f32) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) r[i] += __uint_as_float(res.w[i]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) r[i] += __uint_as_float(i % 2 ? res.w[i / 2] & 0xFFFF0000u : res.w[i / 2] << 16);
     }
+  }
+  if (a.vec) {
     if (a.out_f32)
       *reinterpret_cast<float4*>(reinterpret_cast<float*>(a.out) + at) = make_float4(r[0], r[1], r[2], r[3]);
     else
@@ -88,9 +148,6 @@ __device__ __forceinline__ void epilogue4(const LinearArgs& a, int64_t t, int n,
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     if (n + i >= a.n_out) break;
-    if (a.residual)
-      r[i] += a.res_f32 ? reinterpret_cast<const float*>(a.residual)[at + i]
-                        : bf16_to_f32(reinterpret_cast<const uint16_t*>(a.residual)[at + i]);
     if (a.out_f32)
       reinterpret_cast<float*>(a.out)[at + i] = r[i];
     else

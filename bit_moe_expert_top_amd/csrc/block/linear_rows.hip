@@ -172,7 +172,10 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void linear_rows_kernel(LinearArgs
   for (int i = 0; i < 4; ++i) u[i] = GATED ? __shfl_xor(v[i], 32) : v[i];  // the up row 8 further on
   const int n = n0 + 4 * g;
   if (t >= a.T || n >= a.n_out || (GATED && g >= 2)) return;
-  epilogue4<GATED>(a, t, n, v, u);
+  const int64_t at = t * a.n_out + n;
+  Four res{};
+  if (a.residual) res = load_residual4(a, at, n);
+  epilogue4<GATED>(a, at, n, v, u, load_bias4<GATED>(a, n), res);
 }
 
 template <bool MX, bool GATED, int TT, int NW, int U>
