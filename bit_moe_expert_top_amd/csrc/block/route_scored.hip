@@ -6,6 +6,17 @@
 //   gate = p / sum of the chosen p * scale, or p * scale
 // Ties go to the lower group and the lower expert.  An expert whose c is -inf or NaN is taken
 // after every other and gets gate 0; a group counts its other experts only.
+//
+// The choice has to be that of 64-bit scores, and scores next to each other are told apart only
+// there.  So a token is routed in fp32 with a bound on the error of every comparison that its choice
+// hangs on, and where one is closer than its bound, 64 bits decide: the group sums are formed again,
+// or the candidates (one to a lane) are ranked again.
+//   A lane sorts its E / 64 keys once in registers (a network on the order-preserving 32-bit image of
+//   c, the low bits replaced by the key's place in the lane) and k + 1 rounds of a wave maximum (six
+//   DPP steps) each pop the head of one lane's list: about 20 instructions a round.  The group sums
+//   come from c in LDS, 64 / G lanes to a group.
+// What is left (logits that are not finite, experts out of service among the chosen, more than 64
+// candidates that 64 bits would have to rank) is routed plainly in 64 bits.
 #include "../common.h"
 #include "../route_dev.h"
 #include "block_kernels.h"
@@ -28,89 +39,352 @@ __device__ __forceinline__ int wave_min_i32(int v) {
   return v;
 }
 
-template <int VPL>
-__global__ __launch_bounds__(64 * kRouteWaves) void route_scored_kernel(RouteScoredArgs a) {
-  __shared__ double lds_c[kRouteWaves][64 * VPL];
-  const int lane = wave_lane(), w = threadIdx.x / kWave, E = a.E;
-  for (int64_t t = (int64_t)blockIdx.x * kRouteWaves + w; t < a.T; t += (int64_t)gridDim.x * kRouteWaves) {
-    const float* row = a.logits + t * E;
-    float l[VPL];
-#pragma unroll
-    for (int i = 0; i < VPL; ++i) l[i] = row[min(lane + kWave * i, E - 1)];
-    double lmax = 0.0, inv_sum = 1.0;
-    if (!a.sigmoid) {
-      float m = -__builtin_inff();
-#pragma unroll
-      for (int i = 0; i < VPL; ++i) m = fmaxf(m, l[i]);
-#pragma unroll
-      for (int off = 32; off >= 1; off >>= 1) m = fmaxf(m, __shfl_xor(m, off));
-      lmax = m;
-      double z = 0.0;
-#pragma unroll
-      for (int i = 0; i < VPL; ++i)
-        if (lane + kWave * i < E) z += exp((double)l[i] - lmax);
-      inv_sum = 1.0 / wave_sum(z);
+// ---- One token plainly in 64 bits.  Rare, so it is written for few registers: its values stay in LDS
+// (row: the logits, c_lds: E doubles of this wave) and its loops are not unrolled.
+__device__ void route_token64(const RouteScoredArgs& a, const float* row, int64_t t, double* c_lds) {
+  const int lane = wave_lane(), E = a.E;
+  double lmax = 0.0, inv_sum = 1.0;
+  if (!a.sigmoid) {
+    float m = -__builtin_inff();
+#pragma unroll 1
+    for (int e = lane; e < E; e += kWave) m = fmaxf(m, row[e]);
+#pragma unroll 1
+    for (int off = 32; off >= 1; off >>= 1) m = fmaxf(m, __shfl_xor(m, off));
+    lmax = m;
+    double z = 0.0;
+#pragma unroll 1
+    for (int e = lane; e < E; e += kWave) z += exp((double)row[e] - lmax);
+    inv_sum = 1.0 / wave_sum(z);
+  }
+  auto score = [&](float v) {
+    const double z = exp(a.sigmoid ? -(double)v : (double)v - lmax);
+    return a.sigmoid ? 1.0 / (1.0 + z) : z * inv_sum;
+  };
+#pragma unroll 1
+  for (int e = lane; e < E; e += kWave) {
+    const double c = score(row[e]) + (a.bias ? (double)a.bias[e] : 0.0);
+    c_lds[e] = c > -__builtin_inf() ? c : -__builtin_inf();
+  }
+  __builtin_amdgcn_wave_barrier();
+  uint64_t kept = ~0ull;
+  const int gs = E / a.n_group;
+  if (a.n_group > 1) {
+    double c1 = -__builtin_inf(), c2 = -__builtin_inf();
+    if (lane < a.n_group) {
+#pragma unroll 1
+      for (int j = 0; j < gs; ++j) {
+        const double c = c_lds[lane * gs + j];
+        c2 = fmax(c2, fmin(c, c1));
+        c1 = fmax(c1, c);
+      }
     }
-    auto score = [&](float v) {
-      return a.sigmoid ? 1.0 / (1.0 + exp(-(double)v)) : exp((double)v - lmax) * inv_sum;
-    };
-    uint64_t key[VPL];
+    const double total = a.group_top == 2 && c2 > -__builtin_inf() ? c1 + c2 : c1;
+    int better = 0;
+#pragma unroll 1
+    for (int g = 0; g < a.n_group; ++g) {
+      const double o = __shfl(total, g);
+      better += o > total || (o == total && g < lane);
+    }
+    kept = __ballot(lane < a.n_group && better < a.topk_group);
+  }
+  // c turns into keys in place
+  uint64_t* key = reinterpret_cast<uint64_t*>(c_lds);
+  __builtin_amdgcn_wave_barrier();
+#pragma unroll 1
+  for (int e = lane; e < E; e += kWave) {
+    const double c = c_lds[e];
+    uint64_t v = c > -__builtin_inf() ? order_key64(a.bias ? c : (double)row[e]) : kKeyDead;
+    if (!((kept >> (e / gs & 63)) & 1)) v = 0;
+    key[e] = v;
+  }
+  int mine = 0;
+  bool mine_live = false;
+#pragma unroll 1
+  for (int j = 0; j < a.k; ++j) {
+    uint64_t best = 0;
+#pragma unroll 1
+    for (int e = lane; e < E; e += kWave) best = max_u64(best, key[e]);
+    best = wave_max_u64(best);
+    int win = E;  // the lowest expert with this key
+#pragma unroll 1
+    for (int e = lane; e < E && win == E; e += kWave)
+      if (key[e] == best) win = e;
+    win = wave_min_i32(win);
+    if (lane == (win & 63)) key[win] = 0;
+    __builtin_amdgcn_wave_barrier();
+    if (lane == j) mine = win, mine_live = best > kKeyDead;
+  }
+  double p = 0.0;
+  if (lane < a.k && mine_live) p = score(row[mine]);
+  const double sum = wave_sum(p);
+  if (a.renormalize) p = sum > 0.0 ? p / sum : 0.0;
+  if (lane < a.k) {
+    a.ids[t * a.k + lane] = mine;
+    a.gates[t * a.k + lane] = (float)(p * (double)a.scale);
+  }
+}
+
+// ---- fp32
+template <int CTRL, int ROWS>
+__device__ __forceinline__ uint32_t dpp0(uint32_t v) {  // lanes without a source, and rows left out, get 0
+  return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, ROWS, 0xF, false);
+}
+// Reductions over the wave, the result uniform: exchanges within rows of 16 lanes, then the rows'
+// last lanes carried on (row_bcast 15 into rows 1 and 3, row_bcast 31 into rows 2 and 3).
+template <class Op>
+__device__ __forceinline__ uint32_t wave_reduce(uint32_t v, Op op) {
+  v = op(v, dpp0<0xB1, 0xF>(v));   // quad_perm [1,0,3,2]
+  v = op(v, dpp0<0x4E, 0xF>(v));   // quad_perm [2,3,0,1]
+  v = op(v, dpp0<0x141, 0xF>(v));  // row_half_mirror
+  v = op(v, dpp0<0x140, 0xF>(v));  // row_mirror
+  v = op(v, dpp0<0x142, 0xA>(v));  // row_bcast 15
+  v = op(v, dpp0<0x143, 0xC>(v));  // row_bcast 31
+  return (uint32_t)__builtin_amdgcn_readlane((int)v, 63);
+}
+__device__ __forceinline__ uint32_t wave_max_u32(uint32_t v) {
+  return wave_reduce(v, [](uint32_t a, uint32_t b) { return max(a, b); });
+}
+__device__ __forceinline__ float wave_add_f32(float v) {
+  return __uint_as_float(wave_reduce(__float_as_uint(v), [](uint32_t a, uint32_t b) {
+    return __float_as_uint(__uint_as_float(a) + __uint_as_float(b));
+  }));
+}
+
+// Sorts in descending order by Batcher's merge exchange (Knuth, algorithm 5.2.2M), all indexes
+// constants after unrolling.
+template <int N>
+__device__ __forceinline__ void sort_desc(uint32_t (&v)[N]) {
+  constexpr int kTop = N > 8 ? 8 : N > 4 ? 4 : N > 2 ? 2 : 1;
+#pragma unroll
+  for (int p = kTop; p > 0; p >>= 1) {
+#pragma unroll
+    for (int q = kTop; q >= p; q >>= 1) {
+      const int r = q == kTop ? 0 : p, d = q == kTop ? p : 2 * q - p;
+#pragma unroll
+      for (int i = 0; i + d < N; ++i)
+        if ((i & p) == r) {
+          const uint32_t hi = max(v[i], v[i + d]), lo = min(v[i], v[i + d]);
+          v[i] = hi, v[i + d] = lo;
+        }
+    }
+  }
+}
+
+// Routes one token; false if it is one for route_token64 (nothing is written then).
+// The error of an fp32 score: exp of an argument rounded to fp32 is off by (|x| + 2) 2^-23 of its
+// value; p (1 - p) |l| <= 0.23 for the sigmoid and p |l - max| <= 0.37 for the softmax, whose sum of at
+// most 1024 terms adds (16 + 6) 2^-24, so |error of p| <= 2^-20 for both; adding the bias and dropping
+// B <= 4 bits of c adds (2^-24 + 2^(B - 23)) |c|.  Two scores compare as in 64 bits if they differ by
+// more than twice that, group sums if they differ by more than four times that: kNear covers both.
+template <int VPL>
+__device__ __forceinline__ bool route_token(const RouteScoredArgs& a, const float (&l)[VPL], const float (&bias)[VPL],
+                                            int64_t t, double* c_lds, const float* l_lds) {
+  constexpr int B = VPL > 8 ? 4 : VPL > 4 ? 3 : VPL > 2 ? 2 : VPL > 1 ? 1 : 0;
+  constexpr uint32_t kPlace = (1u << B) - 1;
+  constexpr float kNear = VPL > 8 ? 1.0f / (1 << 17) : 1.0f / (1 << 18);
+  const int lane = wave_lane(), E = a.E;
+  const bool by_logit = !a.bias, grouped = a.n_group > 1;
+  uint32_t key[VPL];
+  float lmax = 0.f, inv_sum = 1.f;
+  {
+    uint32_t m = 0;
+    bool odd = false;  // a NaN or an infinity
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) {
+      key[i] = order_key(l[i]);
+      m = max(m, key[i]);
+      odd |= !(fabsf(l[i]) < __builtin_inff());
+    }
+    if (__ballot(odd)) return false;
+    if (!a.sigmoid) {
+      lmax = key_to_float(wave_max_u32(m));
+      float z = 0.f;
+#pragma unroll
+      for (int i = 0; i < VPL; ++i) z += lane + kWave * i < E ? __expf(l[i] - lmax) : 0.f;
+      inv_sum = 1.0f / wave_add_f32(z);
+    }
+  }
+  auto score = [&](float v) {
+    return a.sigmoid ? __builtin_amdgcn_rcpf(1.0f + __expf(-v)) : __expf(v - lmax) * inv_sum;
+  };
+  // the same in 64 bits; the softmax's sum only when it is needed
+  auto sum64 = [&]() {
+    double z = 0.0;
+    if (!a.sigmoid) {
+#pragma unroll 1
+      for (int e = lane; e < E; e += kWave) z += exp((double)l_lds[e] - (double)lmax);
+      z = 1.0 / wave_sum(z);
+    }
+    return z;
+  };
+  auto score64 = [&](float v, double inv) {
+    const double z = exp(a.sigmoid ? -(double)v : (double)v - (double)lmax);
+    return a.sigmoid ? 1.0 / (1.0 + z) : z * inv;
+  };
+  float* cf_lds = reinterpret_cast<float*>(c_lds);
+  if (by_logit && !grouped) {
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) key[i] = lane + kWave * i < E ? (key[i] & ~kPlace) | i : 0;
+  } else {
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) {
+      const float c = score(l[i]) + bias[i];
+      const bool live = c > -__builtin_inff();
+      if (!by_logit) key[i] = order_key(c);
+      key[i] = lane + kWave * i < E && live ? (key[i] & ~kPlace) | i : 0;
+      if (grouped) cf_lds[lane + kWave * i] = c;
+    }
+  }
+  if (grouped) {
+    // 64 / G' lanes to a group (G' the power of two at or above n_group)
+    const int gs = E / a.n_group, log_g = 32 - __builtin_clz(a.n_group - 1), lanes = 64 >> log_g;
+    const int g = lane >> (6 - log_g);
+    float c1 = -__builtin_inff(), c2 = c1;
+    if (g < a.n_group) {
+      const float* cg = cf_lds + g * gs;
+#pragma unroll 4
+      for (int j = lane & (lanes - 1); j < gs; j += lanes) {
+        const float c = cg[j];
+        c2 = __builtin_amdgcn_fmed3f(c1, c2, c);  // c1 >= c2: the second of the three
+        c1 = fmaxf(c1, c);
+      }
+    }
+    for (int off = 1; off < lanes; off <<= 1) {
+      const float o1 = __shfl_xor(c1, off), o2 = __shfl_xor(c2, off);
+      c2 = fmaxf(fmaxf(c2, o2), fminf(c1, o1));
+      c1 = fmaxf(c1, o1);
+    }
+    const float total = a.group_top == 2 && c2 > -__builtin_inff() ? c1 + c2 : c1;
+    const float near = kNear * (1.0f + fabsf(total));
+    int sure = 0, maybe = -1;  // groups that are better beyond doubt, and that may be (but for itself)
+    const float hi = total + near, lo = total - near;
+    for (int o = 0; o < a.n_group; ++o) {
+      const float other = __uint_as_float(__builtin_amdgcn_readlane((int)__float_as_uint(total), o * lanes));
+      sure += other > hi;
+      maybe += !(other < lo);
+    }
+    bool in = g < a.n_group && maybe < a.topk_group;
+    if (__ballot(!in && g < a.n_group && sure < a.topk_group)) {
+      // too close: the groups' sums in 64 bits
+      const double inv = sum64();
+#pragma unroll 1
+      for (int e = lane; e < E; e += kWave) {
+        const double c = score64(l_lds[e], inv) + (a.bias ? (double)a.bias[e] : 0.0);
+        c_lds[e] = c > -__builtin_inf() ? c : -__builtin_inf();
+      }
+      __builtin_amdgcn_wave_barrier();
+      double d1 = -__builtin_inf(), d2 = d1;
+      if (g < a.n_group) {
+#pragma unroll 1
+        for (int j = lane & (lanes - 1); j < gs; j += lanes) {
+          const double c = c_lds[g * gs + j];
+          d2 = fmax(d2, fmin(d1, c));
+          d1 = fmax(d1, c);
+        }
+      }
+#pragma unroll 1
+      for (int off = 1; off < lanes; off <<= 1) {
+        const double o1 = __shfl_xor(d1, off), o2 = __shfl_xor(d2, off);
+        d2 = fmax(fmax(d2, o2), fmin(d1, o1));
+        d1 = fmax(d1, o1);
+      }
+      const double total64 = a.group_top == 2 && d2 > -__builtin_inf() ? d1 + d2 : d1;
+      int better = 0;
+#pragma unroll 1
+      for (int o = 0; o < a.n_group; ++o) {
+        const double other = __shfl(total64, o * lanes);
+        better += other > total64 || (other == total64 && o < g);
+      }
+      in = g < a.n_group && better < a.topk_group;
+    }
+    const uint64_t kept = __ballot(in);
+    const float inv_gs = 1.0f / (float)gs;
 #pragma unroll
     for (int i = 0; i < VPL; ++i) {
       const int e = lane + kWave * i;
-      const double c = score(l[i]) + (a.bias ? (double)a.bias[min(e, E - 1)] : 0.0);
-      const bool live = c > -__builtin_inf();
-      key[i] = e >= E ? 0 : live ? order_key64(a.bias ? c : (double)l[i]) : kKeyDead;
-      lds_c[w][e] = live ? c : -__builtin_inf();
+      const int eg = (int)(((float)e + 0.5f) * inv_gs);  // e / gs: at least 0.5 / gs from a whole number
+      if (!((kept >> (eg << (6 - log_g) & 63)) & 1)) key[i] = 0;
     }
-    if (a.n_group > 1) {
-      const int gs = E / a.n_group;
-      double c1 = -__builtin_inf(), c2 = -__builtin_inf();
-      if (lane < a.n_group) {
-        for (int j = 0; j < gs; ++j) {
-          const double c = lds_c[w][lane * gs + j];
-          c2 = fmax(c2, fmin(c, c1));
-          c1 = fmax(c1, c);
-        }
-      }
-      const double total = a.group_top == 2 && c2 > -__builtin_inf() ? c1 + c2 : c1;
-      int better = 0;
-      for (int g = 0; g < a.n_group; ++g) {
-        const double o = __shfl(total, g);
-        better += o > total || (o == total && g < lane);
-      }
-      const uint64_t kept = __ballot(lane < a.n_group && better < a.topk_group);
+  }
+  sort_desc(key);
+  // lane j receives the j-th largest key and its lane
+  uint32_t mine = 0, from = 0;
+  auto round = [&](int j) {
+    const uint32_t best = wave_max_u32(key[0]);
+    const int win = __builtin_ctzll(__ballot(key[0] == best));
+    if (lane == j) mine = best, from = win;
+    const bool pop = lane == win;
 #pragma unroll
-      for (int i = 0; i < VPL; ++i) {
-        const int e = lane + kWave * i;
-        if (e < E && !((kept >> (e / gs)) & 1)) key[i] = 0;
-      }
+    for (int i = 0; i + 1 < VPL; ++i) key[i] = pop ? key[i + 1] : key[i];
+    key[VPL - 1] = pop ? 0 : key[VPL - 1];
+    return best;
+  };
+  uint32_t kth = 0, next = 0;
+  for (int j = 0; j < a.k; ++j) kth = round(j);
+  if (kth == 0) return false;
+  int n = a.k;  // candidates
+  // whether key o, at or below key m in order, may be above it in 64 bits (0: no expert)
+  auto close = [&](uint32_t m, uint32_t o) {
+    if (by_logit) return (m & ~kPlace) == (o & ~kPlace);
+    const float c = key_to_float(m & ~kPlace);
+    return o != 0 && !(c - key_to_float(o & ~kPlace) > kNear * (1.0f + fabsf(c)));
+  };
+  next = wave_max_u32(key[0]);
+  const uint32_t below = (uint32_t)__shfl_down((int)mine, 1);
+  int e = (int)(from + kWave * (mine & kPlace));
+  if (close(kth, next) || __ballot(lane < a.k - 1 && close(mine, below))) {
+    // too close: every expert that may be among the k is a candidate, and 64 bits rank them
+    while (close(kth, next)) {
+      if (n == kWave) return false;
+      round(n++);
+      next = wave_max_u32(key[0]);
     }
-    int mine = 0;
-    bool mine_live = false;
-    for (int j = 0; j < a.k; ++j) {
-      uint64_t best = key[0];
-#pragma unroll
-      for (int i = 1; i < VPL; ++i) best = max_u64(best, key[i]);
-      best = wave_max_u64(best);
-      int e = E;  // the lowest expert with this key
-#pragma unroll
-      for (int i = VPL - 1; i >= 0; --i)
-        if (key[i] == best) e = lane + kWave * i;
-      e = wave_min_i32(e);
-#pragma unroll
-      for (int i = 0; i < VPL; ++i)
-        if (lane + kWave * i == e) key[i] = 0;
-      if (lane == j) mine = e, mine_live = best > kKeyDead;
+    const double inv = by_logit ? 0.0 : sum64();
+    e = (int)(from + kWave * (mine & kPlace));
+    double c = -__builtin_inf();
+    if (lane < n) c = by_logit ? (double)l_lds[e] : score64(l_lds[e], inv) + (double)a.bias[e];
+    int rank = 0;
+#pragma unroll 1
+    for (int o = 0; o < n; ++o) {
+      const double oc = __shfl(c, o);
+      const int oe = __builtin_amdgcn_readlane(e, o);
+      rank += oc > c || (oc == c && oe < e);
     }
-    double p = 0.0;
-    if (lane < a.k && mine_live) p = score(row[mine]);
-    const double sum = wave_sum(p);
-    if (a.renormalize) p = sum > 0.0 ? p / sum : 0.0;
-    if (lane < a.k) {
-      a.ids[t * a.k + lane] = mine;
-      a.gates[t * a.k + lane] = (float)(p * (double)a.scale);
+    // lane j takes the candidate of rank j (the ranks of the candidates are a permutation)
+    e = __builtin_amdgcn_ds_permute(4 * (lane < n ? rank : lane), e);
+  }
+  float p = 0.f;
+  if (lane < a.k) p = score(l_lds[e]);
+  const float sum = wave_add_f32(p);
+  if (!(sum > 1e-30f)) return false;  // gates that fp32 does not hold
+  if (a.renormalize) p = p / sum;
+  if (lane < a.k) {
+    a.ids[t * a.k + lane] = e;
+    a.gates[t * a.k + lane] = p * a.scale;
+  }
+  return true;
+}
+
+// At least 4 waves to a SIMD (3 above 512 experts): a token is a long chain of dependent steps, and other
+// tokens fill its gaps.
+template <int VPL>
+__global__ __launch_bounds__(64 * kRouteWaves, VPL > 8 ? 3 : 4) void route_scored_kernel(RouteScoredArgs a) {
+  __shared__ double c_lds[kRouteWaves][64 * VPL];
+  __shared__ float l_lds[kRouteWaves][64 * VPL];
+  const int lane = wave_lane(), w = threadIdx.x / kWave;
+  for (int64_t t = (int64_t)blockIdx.x * kRouteWaves + w; t < a.T; t += (int64_t)gridDim.x * kRouteWaves) {
+    const float* row = a.logits + t * a.E;
+    float l[VPL], bias[VPL];
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) {
+      const int e = min(lane + kWave * i, a.E - 1);
+      l[i] = row[e];
+      bias[i] = a.bias ? a.bias[e] : 0.f;
     }
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) l_lds[w][lane + kWave * i] = l[i];
+    if (!route_token<VPL>(a, l, bias, t, c_lds[w], l_lds[w])) route_token64(a, l_lds[w], t, c_lds[w]);
+    __builtin_amdgcn_wave_barrier();
   }
 }
 
