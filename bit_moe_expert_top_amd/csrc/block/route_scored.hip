@@ -176,27 +176,32 @@ __device__ __forceinline__ void sort_desc(uint32_t (&v)[N]) {
 // most 1024 terms adds (16 + 6) 2^-24, so |error of p| <= 2^-20 for both; adding the bias and dropping
 // B <= 4 bits of c adds (2^-24 + 2^(B - 23)) |c|.  Two scores compare as in 64 bits if they differ by
 // more than twice that, group sums if they differ by more than four times that: kNear covers both.
+// What a lane knows of its experts lane, lane + 64, ... before it sees a token.
 template <int VPL>
-__device__ __forceinline__ bool route_token(const RouteScoredArgs& a, const float (&l)[VPL], const float (&bias)[VPL],
-                                            int64_t t, double* c_lds, const float* l_lds) {
+struct LaneExperts {
+  float bias[VPL];
+  uint32_t group[VPL];  // the first of the group's lanes (see below); 0 for places past the last expert
+};
+
+template <int VPL, bool SIGMOID, bool GROUPED>
+__device__ __forceinline__ bool route_token(const RouteScoredArgs& a, const float (&l)[VPL], const LaneExperts<VPL>& my,
+                                            int log_g, int64_t t, double* c_lds, const float* l_lds) {
   constexpr int B = VPL > 8 ? 4 : VPL > 4 ? 3 : VPL > 2 ? 2 : VPL > 1 ? 1 : 0;
   constexpr uint32_t kPlace = (1u << B) - 1;
   constexpr float kNear = VPL > 8 ? 1.0f / (1 << 17) : 1.0f / (1 << 18);
   const int lane = wave_lane(), E = a.E;
-  const bool by_logit = !a.bias, grouped = a.n_group > 1;
+  const bool by_logit = !a.bias;
   uint32_t key[VPL];
   float lmax = 0.f, inv_sum = 1.f;
   {
-    uint32_t m = 0;
-    bool odd = false;  // a NaN or an infinity
+    float largest = 0.f;  // a NaN or an infinity anywhere makes the sum of l - l a NaN
 #pragma unroll
-    for (int i = 0; i < VPL; ++i) {
-      key[i] = order_key(l[i]);
-      m = max(m, key[i]);
-      odd |= !(fabsf(l[i]) < __builtin_inff());
-    }
-    if (__ballot(odd)) return false;
-    if (!a.sigmoid) {
+    for (int i = 0; i < VPL; ++i) largest += l[i] - l[i];
+    if (__ballot(largest != 0.f)) return false;
+    if (!SIGMOID) {
+      uint32_t m = 0;
+#pragma unroll
+      for (int i = 0; i < VPL; ++i) m = max(m, order_key(l[i]));
       lmax = key_to_float(wave_max_u32(m));
       float z = 0.f;
 #pragma unroll
@@ -205,12 +210,12 @@ __device__ __forceinline__ bool route_token(const RouteScoredArgs& a, const floa
     }
   }
   auto score = [&](float v) {
-    return a.sigmoid ? __builtin_amdgcn_rcpf(1.0f + __expf(-v)) : __expf(v - lmax) * inv_sum;
+    return SIGMOID ? __builtin_amdgcn_rcpf(1.0f + __expf(-v)) : __expf(v - lmax) * inv_sum;
   };
   // the same in 64 bits; the softmax's sum only when it is needed
   auto sum64 = [&]() {
     double z = 0.0;
-    if (!a.sigmoid) {
+    if (!SIGMOID) {
 #pragma unroll 1
       for (int e = lane; e < E; e += kWave) z += exp((double)l_lds[e] - (double)lmax);
       z = 1.0 / wave_sum(z);
@@ -218,26 +223,25 @@ __device__ __forceinline__ bool route_token(const RouteScoredArgs& a, const floa
     return z;
   };
   auto score64 = [&](float v, double inv) {
-    const double z = exp(a.sigmoid ? -(double)v : (double)v - (double)lmax);
-    return a.sigmoid ? 1.0 / (1.0 + z) : z * inv;
+    const double z = exp(SIGMOID ? -(double)v : (double)v - (double)lmax);
+    return SIGMOID ? 1.0 / (1.0 + z) : z * inv;
   };
   float* cf_lds = reinterpret_cast<float*>(c_lds);
-  if (by_logit && !grouped) {
+  if (by_logit && !GROUPED) {
 #pragma unroll
-    for (int i = 0; i < VPL; ++i) key[i] = lane + kWave * i < E ? (key[i] & ~kPlace) | i : 0;
+    for (int i = 0; i < VPL; ++i) key[i] = lane + kWave * i < E ? (order_key(l[i]) & ~kPlace) | i : 0;
   } else {
 #pragma unroll
     for (int i = 0; i < VPL; ++i) {
-      const float c = score(l[i]) + bias[i];
-      const bool live = c > -__builtin_inff();
-      if (!by_logit) key[i] = order_key(c);
-      key[i] = lane + kWave * i < E && live ? (key[i] & ~kPlace) | i : 0;
-      if (grouped) cf_lds[lane + kWave * i] = c;
+      // places past the last expert have a bias of -inf
+      const float c = score(l[i]) + my.bias[i];
+      key[i] = c > -__builtin_inff() ? (order_key(by_logit ? l[i] : c) & ~kPlace) | i : 0;
+      if (GROUPED) cf_lds[lane + kWave * i] = c;
     }
   }
-  if (grouped) {
-    // 64 / G' lanes to a group (G' the power of two at or above n_group)
-    const int gs = E / a.n_group, log_g = 32 - __builtin_clz(a.n_group - 1), lanes = 64 >> log_g;
+  if constexpr (GROUPED) {
+    // 64 / G' lanes to a group (G' = 2^log_g, the power of two at or above n_group)
+    const int gs = E / a.n_group, lanes = 64 >> log_g;
     const int g = lane >> (6 - log_g);
     float c1 = -__builtin_inff(), c2 = c1;
     if (g < a.n_group) {
@@ -298,12 +302,10 @@ __device__ __forceinline__ bool route_token(const RouteScoredArgs& a, const floa
       in = g < a.n_group && better < a.topk_group;
     }
     const uint64_t kept = __ballot(in);
-    const float inv_gs = 1.0f / (float)gs;
 #pragma unroll
     for (int i = 0; i < VPL; ++i) {
-      const int e = lane + kWave * i;
-      const int eg = (int)(((float)e + 0.5f) * inv_gs);  // e / gs: at least 0.5 / gs from a whole number
-      if (!((kept >> (eg << (6 - log_g) & 63)) & 1)) key[i] = 0;
+      const uint32_t half = my.group[i] < 32 ? (uint32_t)kept : (uint32_t)(kept >> 32);
+      key[i] &= (uint32_t)__builtin_amdgcn_sbfe((int)half, my.group[i] & 31, 1);  // all ones or zero
     }
   }
   sort_desc(key);
@@ -365,34 +367,61 @@ __device__ __forceinline__ bool route_token(const RouteScoredArgs& a, const floa
   return true;
 }
 
-// At least 4 waves to a SIMD (3 above 512 experts): a token is a long chain of dependent steps, and other
-// tokens fill its gaps.
-template <int VPL>
+// A wave takes tokens a grid apart; the next token's logits are fetched while this one is routed.  At least
+// 4 waves to a SIMD (3 above 512 experts): a token is a long chain of dependent steps, and other tokens
+// fill its gaps.
+constexpr int kRouteGroups = 1024;  // workgroups of a launch at most: 4 on each of 256 CUs
+template <int VPL, bool SIGMOID, bool GROUPED>
 __global__ __launch_bounds__(64 * kRouteWaves, VPL > 8 ? 3 : 4) void route_scored_kernel(RouteScoredArgs a) {
   __shared__ double c_lds[kRouteWaves][64 * VPL];
   __shared__ float l_lds[kRouteWaves][64 * VPL];
-  const int lane = wave_lane(), w = threadIdx.x / kWave;
-  for (int64_t t = (int64_t)blockIdx.x * kRouteWaves + w; t < a.T; t += (int64_t)gridDim.x * kRouteWaves) {
-    const float* row = a.logits + t * a.E;
-    float l[VPL], bias[VPL];
+  const int lane = wave_lane(), w = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+  const int step = gridDim.x * kRouteWaves;
+  int64_t t = (int64_t)blockIdx.x * kRouteWaves + w;
+  if (t >= a.T) return;
+  float next[VPL];
+  auto fetch = [&](int64_t u) {
+    const float* row = a.logits + u * a.E;
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) next[i] = row[min(lane + kWave * i, a.E - 1)];
+  };
+  fetch(t);
+  LaneExperts<VPL> my;
+  const int log_g = GROUPED ? 32 - __builtin_clz(a.n_group - 1) : 0;
+  const float inv_gs = (float)a.n_group / (float)a.E;
+#pragma unroll
+  for (int i = 0; i < VPL; ++i) {
+    const int e = lane + kWave * i;
+    my.bias[i] = e < a.E ? (a.bias ? a.bias[e] : 0.f) : -__builtin_inff();
+    // e / gs: (e + 1/2) / gs is at least 1 / (2 gs) from a whole number, far more than fp32 loses
+    my.group[i] = GROUPED && e < a.E ? (uint32_t)(((float)e + 0.5f) * inv_gs) << (6 - log_g) : 0;
+  }
+  for (; t < a.T; t += step) {
+    float l[VPL];
 #pragma unroll
     for (int i = 0; i < VPL; ++i) {
-      const int e = min(lane + kWave * i, a.E - 1);
-      l[i] = row[e];
-      bias[i] = a.bias ? a.bias[e] : 0.f;
+      l[i] = next[i];
+      l_lds[w][lane + kWave * i] = l[i];
     }
-#pragma unroll
-    for (int i = 0; i < VPL; ++i) l_lds[w][lane + kWave * i] = l[i];
-    if (!route_token<VPL>(a, l, bias, t, c_lds[w], l_lds[w])) route_token64(a, l_lds[w], t, c_lds[w]);
+    if (t + step < a.T) fetch(t + step);
+    if (!route_token<VPL, SIGMOID, GROUPED>(a, l, my, log_g, t, c_lds[w], l_lds[w]))
+      route_token64(a, l_lds[w], t, c_lds[w]);
     __builtin_amdgcn_wave_barrier();
   }
 }
 
+template <int VPL, bool SIGMOID, bool GROUPED>
+hipError_t start(const RouteScoredArgs& a, hipStream_t s) {
+  const int64_t want = ((int64_t)a.T + kRouteWaves - 1) / kRouteWaves;
+  route_scored_kernel<VPL, SIGMOID, GROUPED>
+      <<<(unsigned)(want < kRouteGroups ? want : kRouteGroups), 64 * kRouteWaves, 0, s>>>(a);
+  return hipGetLastError();
+}
+
 template <int VPL>
 hipError_t go(const RouteScoredArgs& a, hipStream_t s) {
-  const int64_t want = ((int64_t)a.T + kRouteWaves - 1) / kRouteWaves, cap = 1 << 20;
-  route_scored_kernel<VPL><<<(unsigned)(want < cap ? want : cap), 64 * kRouteWaves, 0, s>>>(a);
-  return hipGetLastError();
+  if (a.n_group > 1) return a.sigmoid ? start<VPL, true, true>(a, s) : start<VPL, false, true>(a, s);
+  return a.sigmoid ? start<VPL, true, false>(a, s) : start<VPL, false, false>(a, s);
 }
 
 }  // namespace
