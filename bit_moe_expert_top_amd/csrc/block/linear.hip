@@ -86,7 +86,8 @@ __global__ __launch_bounds__(64 * WM * WN, OCC) void linear_tile_kernel(LinearAr
     const int r = wrow(kRows * (NW * u + w) + prow);
     woff[u] = r < rows_w ? (uint32_t)r * kb_bytes + chunk : kOffNone;
   }
-  // MXFP8: thread j fetches the four scales of stage rows j, j + kThreads, ...
+  // MXFP8: thread j fetches the scales of stage rows j, j + kThreads, ..., those of four stages at a time
+  // (64 lanes read 64 rows: a load costs the same for 4 bytes as for 16; 8192 x 4096 x 2048: 95 -> 88 us)
   constexpr int SR = MX ? (BM + BN + kThreads - 1) / kThreads : 1;
   const uint8_t* scale_row[SR];
   if (MX) {
@@ -102,30 +103,30 @@ __global__ __launch_bounds__(64 * WM * WN, OCC) void linear_tile_kernel(LinearAr
       }
     }
   }
-  uint32_t sreg[S][SR];
+  uint32_t scur[SR][4], snext[SR][4];  // the scales of the four stages in use and of the next four
 
   // the stage buffers by index (a constant wherever they are used)
   auto stage = [&](int d) -> uint8_t* { return d == 0 ? st0 : d == 1 ? st1 : d == 2 ? st2 : d == 3 ? st3 : st4; };
   auto scales = [&](int d) -> uint32_t* { return d == 0 ? sc0 : d == 1 ? sc1 : d == 2 ? sc2 : d == 3 ? sc3 : sc4; };
-  // The scales of stage kb (into a register) and direct load i of UA + UB (the token rows, then the
-  // weight rows) into buffer d.  inner: not the last stage.
-  auto load_scales = [&](int d, int kb, bool inner) {
-    if (!MX) return;
+  // the scales of stages 4 q .. 4 q + 3
+  auto load_scales = [&](uint32_t(&v)[SR][4], int q) {
 #pragma unroll
     for (int c = 0; c < SR; ++c) {
-      uint32_t v = 0;
-      if (scale_row[c]) {
-        const int left = inner ? 4 : K / 32 - 4 * kb;
-        const uint8_t* p = scale_row[c] + 4 * kb;
-        if (left >= 4) {
-          __builtin_memcpy(&v, p, 4);
-        } else {
-          for (int i = 0; i < left; ++i) v |= (uint32_t)p[i] << (8 * i);
-        }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[c][i] = 0;
+      const int left = K / 32 - 16 * q;
+      if (!scale_row[c] || left <= 0) continue;
+      const uint8_t* p = scale_row[c] + 16 * q;
+      if (left >= 16) {
+        __builtin_memcpy(v[c], p, 16);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 15; ++i)
+          if (i < left) v[c][i / 4] |= (uint32_t)p[i] << (8 * (i % 4));
       }
-      sreg[d][c] = v;
     }
   };
+  // Direct load i of UA + UB (the token rows, then the weight rows) of stage kb into buffer d.
   auto load_one = [&](int d, int kb, int i, bool in) {
     const bool is_x = i < UA;
     uint8_t* dst = stage(d) + (is_x ? 1024 * (NW * i + w) : BM * kRow + 1024 * (NW * (i - UA) + w));
@@ -133,9 +134,8 @@ __global__ __launch_bounds__(64 * WM * WN, OCC) void linear_tile_kernel(LinearAr
     __builtin_amdgcn_raw_ptr_buffer_load_lds(is_x ? rx : rw, (lds_void*)dst, 16, (int)(in ? off : kOffNone), kb * kRow,
                                              0, 0);
   };
-  // the first n direct loads of a stage
+  // the first n direct loads of a stage; inner: not the last stage
   auto load = [&](int d, int kb, bool inner, int n) {
-    load_scales(d, kb, inner);
     // a chunk is all inside its row or all outside
     const bool in = inner || !tail || kb < nk - 1 || kb * kRow + (int)chunk < kb_bytes;
 #pragma unroll
@@ -190,11 +190,26 @@ __global__ __launch_bounds__(64 * WM * WN, OCC) void linear_tile_kernel(LinearAr
   using I2 = std::integral_constant<int, 2>;
   using I3 = std::integral_constant<int, 3>;
   using I4 = std::integral_constant<int, 4>;
-  auto put_scales = [&](int d) {
+  // the scales of stage kb, the stages in turn, into buffer d
+  auto put_scales = [&](int d, int kb) {
+    if (!MX) return;
+    const int i = kb & 3;
 #pragma unroll
     for (int c = 0; c < SR; ++c)
-      if (MX && tid + c * kThreads < BM + BN) scales(d)[tid + c * kThreads] = sreg[d][c];
+      if (tid + c * kThreads < BM + BN)
+        scales(d)[tid + c * kThreads] = i == 0 ? scur[c][0] : i == 1 ? scur[c][1] : i == 2 ? scur[c][2] : scur[c][3];
+    if (i == 3) {
+#pragma unroll
+      for (int c = 0; c < SR; ++c)
+#pragma unroll
+        for (int b = 0; b < 4; ++b) scur[c][b] = snext[c][b];
+      load_scales(snext, kb / 4 + 2);
+    }
   };
+  if (MX) {
+    load_scales(scur, 0);
+    load_scales(snext, 1);
+  }
   // Stages 0 .. S - 1; of the last one only the first part of kSpread, the others are fetched by step 0.
   if (nk > S) {
 #pragma unroll
@@ -206,7 +221,7 @@ __global__ __launch_bounds__(64 * WM * WN, OCC) void linear_tile_kernel(LinearAr
       if (d < nk) load(d, d, false, d < S - 1 ? LD : LD / kSpread);
     wait_vm<0, false>();
   }
-  put_scales(0);
+  put_scales(0, 0);
   wait_vm<63, true>();
   asm volatile("s_barrier" ::: "memory");
   Ops op[2];
@@ -240,10 +255,9 @@ __global__ __launch_bounds__(64 * WM * WN, OCC) void linear_tile_kernel(LinearAr
           wait_vm<(S - 2) * LD, false>();
         else
           wait_vm<0, false>();
-        put_scales(next);
+        put_scales(next, kb + 1);
         wait_vm<63, true>();
         asm volatile("s_barrier" ::: "memory");
-        if (refill) load_scales(fd, fk, kMain);
       }
 #pragma unroll
       for (int t = 0; t < AT; ++t) {
@@ -342,7 +356,7 @@ __global__ __launch_bounds__(64 * WM * WN, OCC) void linear_tile_kernel(LinearAr
       const float4 u4 = GATED ? *reinterpret_cast<const float4*>(get + i * kStep * kPitch + 16) : v4;
       const float v[4] = {v4.x, v4.y, v4.z, v4.w}, u[4] = {u4.x, u4.y, u4.z, u4.w};
       if (32 * t + i * kStep < rows)
-        epilogue4<GATED>(a, at0 + (int64_t)(32 * t + i * kStep) * a.n_out, n, v, u, bias, now[i]);
+        epilogue4<GATED, (BM * BN > 64 * 64)>(a, at0 + (int64_t)(32 * t + i * kStep) * a.n_out, n, v, u, bias, now[i]);
     }
     __builtin_amdgcn_wave_barrier();
   }
@@ -360,9 +374,7 @@ hipError_t go_tile(const LinearArgs& a, hipStream_t s) {
 template <bool MX, bool GATED>
 hipError_t launch(const LinearArgs& a, hipStream_t s) {
   auto tiles = [&](int bm, int bn) { return (((int64_t)a.T + bm - 1) / bm) * ((a.N + bn - 1) / bn); };
-  if constexpr (MX) {
-    if (tiles(256, 128) >= 256) return go_tile<MX, GATED, 256, 128, 4, 2, 2, 2, 128, 1>(a, s);
-  } else {
+  if constexpr (!MX) {
     if (tiles(256, 256) >= 128) return go_tile<MX, GATED, 256, 256, 2, 4, 2, 2, 128, 2>(a, s);
   }
   if (tiles(128, 128) >= 192) return go_tile<MX, GATED, 128, 128, 2, 2, 2, 2, 128, 1>(a, s);

@@ -7,6 +7,7 @@
 namespace bitmoe {
 
 typedef float f32x16_t __attribute__((ext_vector_type(16)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 
 // D(32x32, f32) += A(32x16, bf16) * B(16x32, bf16): lane l supplies A row l % 32 and B column l % 32
 // for k = 8 (l / 32) .. + 7 and receives D[8 (j / 4) + 4 (l / 32) + j % 4][l % 32] in register j.
@@ -115,8 +116,10 @@ __device__ __forceinline__ FourBias load_bias4(const LinearArgs& a, int n) {
 }
 
 // v (and, with SwiGLU, the up columns u): the sums without bias.  Adds the bias, applies the
-// activation, adds the residual and stores, rounding once.
-template <bool GATED>
+// activation, adds the residual and stores, rounding once.  STREAM: non-temporal stores, for outputs
+// that are larger than the caches (8192 x 4096 bf16 of K = 4096: 221 -> 209 us, of MXFP8 K = 2048 with a
+// residual: 114 -> 100 us; non-temporal loads of the residual cost 8 us).
+template <bool GATED, bool STREAM>
 __device__ __forceinline__ void epilogue4(const LinearArgs& a, int64_t at, int n, const float (&v)[4],
                                           const float (&u)[4], const FourBias& bias, const Four& res) {
   float r[4];
@@ -138,11 +141,21 @@ __device__ __forceinline__ void epilogue4(const LinearArgs& a, int64_t at, int n
     }
   }
   if (a.vec) {
-    if (a.out_f32)
-      *reinterpret_cast<float4*>(reinterpret_cast<float*>(a.out) + at) = make_float4(r[0], r[1], r[2], r[3]);
-    else
-      *reinterpret_cast<uint2*>(reinterpret_cast<uint16_t*>(a.out) + at) =
-          make_uint2(f32x2_to_bf16x2_rne(r[0], r[1]), f32x2_to_bf16x2_rne(r[2], r[3]));
+    if (a.out_f32) {
+      f32x4* o = reinterpret_cast<f32x4*>(reinterpret_cast<float*>(a.out) + at);
+      const f32x4 q = {r[0], r[1], r[2], r[3]};
+      if (STREAM)
+        __builtin_nontemporal_store(q, o);
+      else
+        *o = q;
+    } else {
+      u32x2* o = reinterpret_cast<u32x2*>(reinterpret_cast<uint16_t*>(a.out) + at);
+      const u32x2 q = {f32x2_to_bf16x2_rne(r[0], r[1]), f32x2_to_bf16x2_rne(r[2], r[3])};
+      if (STREAM)
+        __builtin_nontemporal_store(q, o);
+      else
+        *o = q;
+    }
     return;
   }
 #pragma unroll

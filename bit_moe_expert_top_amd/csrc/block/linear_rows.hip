@@ -175,7 +175,7 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void linear_rows_kernel(LinearArgs
   const int64_t at = t * a.n_out + n;
   Four res{};
   if (a.residual) res = load_residual4(a, at, n);
-  epilogue4<GATED>(a, at, n, v, u, load_bias4<GATED>(a, n), res);
+  epilogue4<GATED, false>(a, at, n, v, u, load_bias4<GATED>(a, n), res);
 }
 
 template <bool MX, bool GATED, int TT, int NW, int U>

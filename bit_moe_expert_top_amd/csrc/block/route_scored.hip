@@ -370,7 +370,7 @@ __device__ __forceinline__ bool route_token(const RouteScoredArgs& a, const floa
 // A wave takes tokens a grid apart; the next token's logits are fetched while this one is routed.  At least
 // 4 waves to a SIMD (3 above 512 experts): a token is a long chain of dependent steps, and other tokens
 // fill its gaps.
-constexpr int kRouteGroups = 1024;  // workgroups of a launch at most: 4 on each of 256 CUs
+constexpr int kRouteGroups = 2048;  // workgroups of a launch at most: two rounds of 4 on each of 256 CUs
 template <int VPL, bool SIGMOID, bool GROUPED>
 __global__ __launch_bounds__(64 * kRouteWaves, VPL > 8 ? 3 : 4) void route_scored_kernel(RouteScoredArgs a) {
   __shared__ double c_lds[kRouteWaves][64 * VPL];
