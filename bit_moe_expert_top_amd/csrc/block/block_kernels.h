@@ -53,8 +53,8 @@ struct LinearArgs {
   int res_f32, out_f32;
   int vec;  // rows of out and residual allow 4-column vector accesses
 };
-// few token rows (linear_rows.hip)
-hipError_t launch_linear_rows(const LinearArgs& a, bool mxfp8, hipStream_t s);
+// few token rows (linear_rows.hip): 16 tt of them to a workgroup, tt = 1, 2 or 4
+hipError_t launch_linear_rows(const LinearArgs& a, bool mxfp8, int tt, hipStream_t s);
 hipError_t launch_linear(const LinearArgs& a, bool mxfp8, hipStream_t s);
 
 }  // namespace bitmoe

@@ -23,9 +23,9 @@ namespace bitmoe {
 namespace {
 
 constexpr int kXcds = 8;
-template <bool MX, bool GATED, int BM, int BN, int WM, int WN, int S, int OCC, int kRow, int kSpread>
-__global__ __launch_bounds__(64 * WM * WN, OCC) void linear_tile_kernel(LinearArgs a, int m_tiles, int n_tiles) {
-  constexpr int NW = WM * WN, kThreads = 64 * NW;
+template <bool MX, bool GATED, int BM, int BN, int WM, int WN, int WK, int S, int OCC, int kRow, int kSpread>
+__global__ __launch_bounds__(64 * WM * WN * WK, OCC) void linear_tile_kernel(LinearArgs a, int m_tiles, int n_tiles) {
+  constexpr int NW = WM * WN, kThreads = 64 * NW;      // of one K group
   constexpr int AT = BM / WM / 32, BT = BN / WN / 32;   // token and weight MFMA tiles of a wave
   constexpr int kEs = MX ? 1 : 2, kStepK = kRow / kEs;
   constexpr int kCh = MX ? 2 : 1;                       // 16-byte chunks of a lane per operand and sub-step
@@ -35,18 +35,21 @@ __global__ __launch_bounds__(64 * WM * WN, OCC) void linear_tile_kernel(LinearAr
   constexpr int LD = UA + UB;  // direct loads per wave and stage (the waits below count at least these)
   constexpr int kStage = (BM + BN) * kRow, kScale = MX ? BM + BN : 4;
   static_assert(LD % (kSpread * AT) == 0 || kSpread == 1, "refill parts");
-  static_assert(S >= 2 && S <= 5 && (kRow == 128 || (kRow == 64 && !MX)), "ring");
+  static_assert(S >= 2 && S <= 4 && (WK == 1 || WK == 2) && (kRow == 128 || (kRow == 64 && !MX)), "ring");
   static_assert(BM % (kRows * NW) == 0 && BN % (kRows * NW) == 0 && NW % 4 == 0 , "loads");
   // one object per stage: the compiler tracks direct loads per object, so a read of one stage does
   // not wait for another's
-  __shared__ __align__(16) uint8_t st0[kStage], st1[kStage], st2[S > 2 ? kStage : 16], st3[S > 3 ? kStage : 16],
-      st4[S > 4 ? kStage : 16];
-  __shared__ uint32_t sc0[kScale], sc1[kScale], sc2[S > 2 ? kScale : 4], sc3[S > 3 ? kScale : 4], sc4[S > 4 ? kScale : 4];
-  const int tid = threadIdx.x, lane = wave_lane();
+  __shared__ __align__(16) uint8_t st0[WK * kStage], st1[WK * kStage], st2[S > 2 ? WK * kStage : 16],
+      st3[S > 3 ? WK * kStage : 16];
+  __shared__ uint32_t sc0[WK * kScale], sc1[WK * kScale], sc2[S > 2 ? WK * kScale : 4], sc3[S > 3 ? WK * kScale : 4];
+  const int tid = threadIdx.x % kThreads, lane = wave_lane();
   const int w = __builtin_amdgcn_readfirstlane(tid / kWave);
+  const int group = WK == 1 ? 0 : __builtin_amdgcn_readfirstlane(threadIdx.x / kThreads);
   const int wm = w % WM, wn = w / WM, r32 = lane & 31, hl = lane >> 5;
-  const int K = a.K, kb_bytes = K * kEs, nk = (K + kStepK - 1) / kStepK;
-  const bool tail = K % kStepK != 0;
+  const int K = a.K, kb_bytes = K * kEs, nk = ((K + kStepK - 1) / kStepK + WK - 1) / WK;
+  // the group's steps are the row's steps first_step + [0, nk); what lies past K is zeros
+  const int first_step = group * nk;
+  const bool tail = WK > 1 || K % kStepK != 0;
 
   // Workgroups go to the 8 XCDs round robin.  Each XCD takes a contiguous run of tiles, ordered in
   // bands of 8 token tiles, column by column, so that the tiles running on it at a time share their
@@ -106,17 +109,17 @@ __global__ __launch_bounds__(64 * WM * WN, OCC) void linear_tile_kernel(LinearAr
   uint32_t scur[SR][4], snext[SR][4];  // the scales of the four stages in use and of the next four
 
   // the stage buffers by index (a constant wherever they are used)
-  auto stage = [&](int d) -> uint8_t* { return d == 0 ? st0 : d == 1 ? st1 : d == 2 ? st2 : d == 3 ? st3 : st4; };
-  auto scales = [&](int d) -> uint32_t* { return d == 0 ? sc0 : d == 1 ? sc1 : d == 2 ? sc2 : d == 3 ? sc3 : sc4; };
+  auto stage = [&](int d) -> uint8_t* { return (d == 0 ? st0 : d == 1 ? st1 : d == 2 ? st2 : st3) + group * kStage; };
+  auto scales = [&](int d) -> uint32_t* { return (d == 0 ? sc0 : d == 1 ? sc1 : d == 2 ? sc2 : sc3) + group * kScale; };
   // the scales of stages 4 q .. 4 q + 3
   auto load_scales = [&](uint32_t(&v)[SR][4], int q) {
 #pragma unroll
     for (int c = 0; c < SR; ++c) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) v[c][i] = 0;
-      const int left = K / 32 - 16 * q;
+      const int left = K / 32 - 4 * first_step - 16 * q;
       if (!scale_row[c] || left <= 0) continue;
-      const uint8_t* p = scale_row[c] + 16 * q;
+      const uint8_t* p = scale_row[c] + 4 * first_step + 16 * q;
       if (left >= 16) {
         __builtin_memcpy(v[c], p, 16);
       } else {
@@ -131,13 +134,13 @@ __global__ __launch_bounds__(64 * WM * WN, OCC) void linear_tile_kernel(LinearAr
     const bool is_x = i < UA;
     uint8_t* dst = stage(d) + (is_x ? 1024 * (NW * i + w) : BM * kRow + 1024 * (NW * (i - UA) + w));
     const uint32_t off = is_x ? xoff[is_x ? i : 0] : woff[is_x ? 0 : i - UA];
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(is_x ? rx : rw, (lds_void*)dst, 16, (int)(in ? off : kOffNone), kb * kRow,
-                                             0, 0);
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(is_x ? rx : rw, (lds_void*)dst, 16, (int)(in ? off : kOffNone),
+                                             (first_step + kb) * kRow, 0, 0);
   };
   // the first n direct loads of a stage; inner: not the last stage
   auto load = [&](int d, int kb, bool inner, int n) {
     // a chunk is all inside its row or all outside
-    const bool in = inner || !tail || kb < nk - 1 || kb * kRow + (int)chunk < kb_bytes;
+    const bool in = (WK == 1 && inner) || !tail || (first_step + kb) * kRow + (int)chunk < kb_bytes;
 #pragma unroll
     for (int i = 0; i < LD; ++i)
       if (i < n) load_one(d, kb, i, in);
@@ -181,15 +184,18 @@ __global__ __launch_bounds__(64 * WM * WN, OCC) void linear_tile_kernel(LinearAr
       else
         acc[t][b] = mfma_bf16_32x32x16(o.w[b][0], o.x[t][0], acc[t][b]);
     }
+    // The largest tile keeps its sums in the ordinary registers; there the compiler is held to issue
+    // these MFMAs here (8192 x 4096 x 4096: 212 -> 207 us).
+    if constexpr (AT * BT == 8) {
 #pragma unroll
-    for (int b = 0; b < BT; ++b) hold<(AT * BT > 8)>(acc[t][b]);
+      for (int b = 0; b < BT; ++b) hold(acc[t][b]);
+    }
   };
 
   using I0 = std::integral_constant<int, 0>;
   using I1 = std::integral_constant<int, 1>;
   using I2 = std::integral_constant<int, 2>;
   using I3 = std::integral_constant<int, 3>;
-  using I4 = std::integral_constant<int, 4>;
   // the scales of stage kb, the stages in turn, into buffer d
   auto put_scales = [&](int d, int kb) {
     if (!MX) return;
@@ -248,7 +254,7 @@ __global__ __launch_bounds__(64 * WM * WN, OCC) void linear_tile_kernel(LinearAr
       const int p = last ? 0 : j + 1, fd = last ? d : (d + S - 1) % S, fk = last ? kb + S : kb - 1 + S;
       static_assert(kSpread <= kSub, "a refill ends before the next step's barrier");
       const bool refill = p < kSpread && (kMain || fk < nk);
-      const bool in = kMain || !tail || fk < nk - 1 || fk * kRow + (int)chunk < kb_bytes;
+      const bool in = (WK == 1 && kMain) || !tail || (first_step + fk) * kRow + (int)chunk < kb_bytes;
       if (last && more) {
         // this wave's loads of the next stage have landed (those of later ones may be in flight)
         if (kMain || kb + S <= nk)
@@ -290,7 +296,6 @@ __global__ __launch_bounds__(64 * WM * WN, OCC) void linear_tile_kernel(LinearAr
     step(I1{}, std::true_type{}, kb + 1);
     if constexpr (S > 2) step(I2{}, std::true_type{}, kb + 2);
     if constexpr (S > 3) step(I3{}, std::true_type{}, kb + 3);
-    if constexpr (S > 4) step(I4{}, std::true_type{}, kb + 4);
   }
   // at most 2 S steps are left
 #pragma unroll
@@ -301,8 +306,35 @@ __global__ __launch_bounds__(64 * WM * WN, OCC) void linear_tile_kernel(LinearAr
       if (kb + 2 < nk) step(I2{}, std::false_type{}, kb + 2);
     if constexpr (S > 3)
       if (kb + 3 < nk) step(I3{}, std::false_type{}, kb + 3);
-    if constexpr (S > 4)
-      if (kb + 4 < nk) step(I4{}, std::false_type{}, kb + 4);
+  }
+
+  if constexpr (WK == 2) {
+    // the second group's sums join the first's through its own buffers
+    static_assert(NW * 64 * 16 * AT * BT * 4 <= kStage, "join");
+    f32x4* join = reinterpret_cast<f32x4*>(st0 + kStage) + tid;
+    __syncthreads();
+    if (group == 1) {
+#pragma unroll
+      for (int t = 0; t < AT; ++t)
+#pragma unroll
+        for (int b = 0; b < BT; ++b)
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            join[((t * BT + b) * 4 + q) * kThreads] =
+                f32x4{acc[t][b][4 * q], acc[t][b][4 * q + 1], acc[t][b][4 * q + 2], acc[t][b][4 * q + 3]};
+    }
+    __syncthreads();
+    if (group == 1) return;
+#pragma unroll
+    for (int t = 0; t < AT; ++t)
+#pragma unroll
+      for (int b = 0; b < BT; ++b)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const f32x4 v = join[((t * BT + b) * 4 + q) * kThreads];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) acc[t][b][4 * q + i] += v[i];
+        }
   }
 
   // ---- epilogue: 32 token rows of the wave at a time through the wave's part of the stages (rows of
@@ -325,7 +357,7 @@ __global__ __launch_bounds__(64 * WM * WN, OCC) void linear_tile_kernel(LinearAr
     }
   };
   fetch(0);
-  __syncthreads();
+  if constexpr (WK == 1) __syncthreads();  // all waves have read the last stage
   constexpr int kFit = kStage / (32 * kPitch * 4);  // waves whose part fits one stage
   static_assert((NW + kFit - 1) / kFit <= S, "epilogue staging");
   float* ep = reinterpret_cast<float*>(stage(w / kFit)) + w % kFit * 32 * kPitch;
@@ -362,24 +394,70 @@ __global__ __launch_bounds__(64 * WM * WN, OCC) void linear_tile_kernel(LinearAr
   }
 }
 
-template <bool MX, bool GATED, int BM, int BN, int WM, int WN, int S, int OCC, int kRow, int kSpread>
+template <bool MX, bool GATED, int BM, int BN, int WM, int WN, int WK, int S, int OCC, int kRow, int kSpread>
 hipError_t go_tile(const LinearArgs& a, hipStream_t s) {
   const int64_t m_tiles = ((int64_t)a.T + BM - 1) / BM;
   const int bn = GATED ? BN / 2 : BN, n_tiles = (a.n_out + bn - 1) / bn;
-  linear_tile_kernel<MX, GATED, BM, BN, WM, WN, S, OCC, kRow, kSpread>
-      <<<(unsigned)(m_tiles * n_tiles), 64 * WM * WN, 0, s>>>(a, (int)m_tiles, n_tiles);
+  linear_tile_kernel<MX, GATED, BM, BN, WM, WN, WK, S, OCC, kRow, kSpread>
+      <<<(unsigned)(m_tiles * n_tiles), 64 * WM * WN * WK, 0, s>>>(a, (int)m_tiles, n_tiles);
   return hipGetLastError();
+}
+
+// Which kernel: the one whose launch takes the least time by its rounds, a round being the workgroups
+// that run at once (one or two to a CU).  The times of a round were measured at K = 4096 (us, by HIP
+// graph replays; every variant's time grows with K alike):
+//   token rows x weight rows   at once    bf16    MXFP8
+//   16 x 16  (linear_rows)     256         8.2     6.1
+//   32 x 16  (linear_rows)     256         9.7     7.0
+//   64 x 16  (linear_rows)     256        12.7     9.8
+//   64 x 64                    256        14.5    18.5 (15.1 with K split over two groups of waves)
+//   64 x 64                    512        29      21.7
+//   64 x 128, four stages      256        23.5    (23.2: never the least)
+//   128 x 128, four stages     256        36      (28.8: never the least)
+//   128 x 128                  512        67      41 (30.5 for 256)
+//   256 x 256                  256       105      -  (does not fit the registers)
+// e.g. bf16 of 1001 x 4096: 128 x 128 with four stages 38 us, 64 x 64 55 us; 2048 x 4096: 128 x 128 67 us,
+// 64 x 128 89 us; 192 x 1024: 64 x 16 11.3 us, 64 x 64 14.5 us.
+enum Variant { kRows16, kRows32, kRows64, kTile64, kTile64Split, kTile64x128, kTile128Deep, kTile128, kTile256 };
+template <bool MX>
+Variant choose(const LinearArgs& a) {
+  Variant best = kRows16;
+  double least = 1e30;
+  auto consider = [&](Variant v, int bm, int bn, int at_once, double round) {
+    const int64_t n = (((int64_t)a.T + bm - 1) / bm) * (((int64_t)a.N + bn - 1) / bn);
+    const double t = (double)((n + at_once - 1) / at_once) * round;
+    if (t < least) least = t, best = v;
+  };
+  consider(kRows16, 16, 16, 256, MX ? 6.1 : 8.2);
+  consider(kRows32, 32, 16, 256, MX ? 7.0 : 9.7);
+  consider(kRows64, 64, 16, 256, MX ? 9.8 : 12.7);
+  if (MX) {
+    consider(kTile64Split, 64, 64, 256, 15.1);
+    consider(kTile64, 64, 64, 512, 21.7);
+    consider(kTile128, 128, 128, 256, 30.5);
+    consider(kTile128, 128, 128, 512, 41.0);
+  } else {
+    consider(kTile64, 64, 64, 256, 14.5);
+    consider(kTile64x128, 64, 128, 256, 23.5);
+    consider(kTile128Deep, 128, 128, 256, 36.0);
+    consider(kTile128, 128, 128, 512, 67.0);
+    consider(kTile256, 256, 256, 256, 105.0);
+  }
+  return best;
 }
 
 template <bool MX, bool GATED>
 hipError_t launch(const LinearArgs& a, hipStream_t s) {
-  auto tiles = [&](int bm, int bn) { return (((int64_t)a.T + bm - 1) / bm) * ((a.N + bn - 1) / bn); };
+  const Variant v = choose<MX>(a);
+  if (v <= kRows64) return launch_linear_rows(a, MX, v == kRows16 ? 1 : v == kRows32 ? 2 : 4, s);
+  if (v == kTile64) return go_tile<MX, GATED, 64, 64, 2, 2, 1, 4, 2, 128, 1>(a, s);
+  if (v == kTile128) return go_tile<MX, GATED, 128, 128, 2, 2, 1, 2, 2, 128, 1>(a, s);
+  if constexpr (MX) return go_tile<MX, GATED, 64, 64, 2, 2, 2, 4, 2, 128, 1>(a, s);
   if constexpr (!MX) {
-    if (tiles(256, 256) >= 128) return go_tile<MX, GATED, 256, 256, 2, 4, 2, 2, 128, 2>(a, s);
+    if (v == kTile64x128) return go_tile<MX, GATED, 64, 128, 2, 2, 1, 4, 2, 128, 1>(a, s);
+    if (v == kTile128Deep) return go_tile<MX, GATED, 128, 128, 2, 2, 1, 4, 1, 128, 1>(a, s);
+    return go_tile<MX, GATED, 256, 256, 2, 4, 1, 2, 2, 128, 2>(a, s);
   }
-  if (tiles(128, 128) >= 192) return go_tile<MX, GATED, 128, 128, 2, 2, 2, 2, 128, 1>(a, s);
-  if (a.T > 64 && tiles(64, 64) >= 64) return go_tile<MX, GATED, 64, 64, 2, 2, 4, 2, 128, 1>(a, s);
-  return launch_linear_rows(a, MX, s);
 }
 
 }  // namespace

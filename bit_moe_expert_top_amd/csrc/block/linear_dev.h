@@ -33,16 +33,10 @@ __device__ __forceinline__ void wait_vm() {
   __builtin_amdgcn_s_waitcnt((N & 15) | 0x70 | (LGKM ? 0 : 0xF00) | ((N >> 4) << 14));
 }
 
-// The MFMA builtins are pure: an empty volatile asm that reads their results keeps them from sinking
-// past the reads and barriers that follow.
-// ACC: accumulation registers (kernels whose sums leave no room in the others).
-template <bool ACC>
+// An empty asm that reads a result in ordinary registers: what computes it is not moved past.
 __device__ __forceinline__ void hold(const f32x16_t& v) {
 #if defined(__HIP_DEVICE_COMPILE__)
-  if constexpr (ACC)
-    asm volatile("" ::"a"(v));
-  else
-    asm volatile("" ::"v"(v));
+  asm volatile("" ::"v"(v));
 #endif
 }
 

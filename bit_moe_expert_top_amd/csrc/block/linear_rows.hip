@@ -187,20 +187,18 @@ hipError_t go_rows(const LinearArgs& a, hipStream_t s) {
 }
 
 template <bool MX, bool GATED>
-hipError_t launch(const LinearArgs& a, hipStream_t s) {
-  const int64_t n_tiles = (a.n_out + (GATED ? 7 : 15)) / (GATED ? 8 : 16);
-  // the most tokens per workgroup (each reads all of its weight rows) that still give every CU one
-  if (a.T > 32 && ((int64_t)a.T + 63) / 64 * n_tiles >= 256) return go_rows<MX, GATED, 4, 4, 3>(a, s);
-  if (a.T > 16 && ((int64_t)a.T + 31) / 32 * n_tiles >= 256) return go_rows<MX, GATED, 2, 8, 3>(a, s);
-  return go_rows<MX, GATED, 1, 8, 4>(a, s);
+hipError_t launch(const LinearArgs& a, int tt, hipStream_t s) {
+  if (tt == 1) return go_rows<MX, GATED, 1, 8, 4>(a, s);
+  if (tt == 2) return go_rows<MX, GATED, 2, 8, 3>(a, s);
+  return go_rows<MX, GATED, 4, 4, 3>(a, s);
 }
 
 }  // namespace
 
-hipError_t launch_linear_rows(const LinearArgs& a, bool mxfp8, hipStream_t s) {
+hipError_t launch_linear_rows(const LinearArgs& a, bool mxfp8, int tt, hipStream_t s) {
   const bool gated = a.act == kActSwiglu;
-  if (mxfp8) return gated ? launch<true, true>(a, s) : launch<true, false>(a, s);
-  return gated ? launch<false, true>(a, s) : launch<false, false>(a, s);
+  if (mxfp8) return gated ? launch<true, true>(a, tt, s) : launch<true, false>(a, tt, s);
+  return gated ? launch<false, true>(a, tt, s) : launch<false, false>(a, tt, s);
 }
 
 }  // namespace bitmoe
