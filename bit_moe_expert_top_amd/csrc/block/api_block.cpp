@@ -14,7 +14,8 @@ namespace {
 constexpr int kMaxE = 1024;
 constexpr int kMaxTopK = 64;
 constexpr int kMaxGroups = 64;
-constexpr int kMaxLinear = 1 << 20;  // N and K
+constexpr int kMaxLinear = 1 << 20;    // N and K
+constexpr int kMaxLinearRows = 1 << 26;  // T: a launch has fewer than 2^32 threads
 
 inline hipStream_t as_stream(void* s) { return reinterpret_cast<hipStream_t>(s); }
 inline moe_status from_hip(hipError_t e) { return e == hipSuccess ? MOE_OK : MOE_ERR_HIP; }
@@ -89,7 +90,7 @@ moe_status moe_linear(const void* x, const uint8_t* x_scales, const void* w, con
     return MOE_ERR_INVALID_ARG;
   const bool mx = dtype == MOE_DT_MXFP8, gated = act == MOE_ACT_SWIGLU;
   if ((mx && K % 32) || (gated && N % 2)) return MOE_ERR_INVALID_ARG;
-  if (K % 8 || N > kMaxLinear || K > kMaxLinear || (mx && out_dtype == MOE_DT_F32)) return MOE_ERR_UNSUPPORTED;
+  if (K % 8 || N > kMaxLinear || K > kMaxLinear || T > kMaxLinearRows || (mx && out_dtype == MOE_DT_F32)) return MOE_ERR_UNSUPPORTED;
   if (T == 0) return MOE_OK;
   if (!x || !w || !out || (mx && (!x_scales || !w_scales))) return MOE_ERR_INVALID_ARG;
   const size_t ob = out_dtype == MOE_DT_F32 ? 4 : 2, rb = residual_dtype == MOE_DT_F32 ? 4 : 2;

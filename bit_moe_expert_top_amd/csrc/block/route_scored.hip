@@ -25,6 +25,10 @@ namespace bitmoe {
 
 namespace {
 
+// LDS words that hold values of more than one type in turn
+typedef float __attribute__((may_alias)) aliased_float;
+typedef uint64_t __attribute__((may_alias)) aliased_u64;
+
 constexpr int kRouteWaves = 4;
 constexpr uint64_t kKeyDead = 1;  // below the key of every selectable expert; 0: not available
 
@@ -88,7 +92,7 @@ __device__ void route_token64(const RouteScoredArgs& a, const float* row, int64_
     kept = __ballot(lane < a.n_group && better < a.topk_group);
   }
   // c turns into keys in place
-  uint64_t* key = reinterpret_cast<uint64_t*>(c_lds);
+  aliased_u64* key = reinterpret_cast<aliased_u64*>(c_lds);
   __builtin_amdgcn_wave_barrier();
 #pragma unroll 1
   for (int e = lane; e < E; e += kWave) {
@@ -226,7 +230,7 @@ __device__ __forceinline__ bool route_token(const RouteScoredArgs& a, const floa
     const double z = exp(SIGMOID ? -(double)v : (double)v - (double)lmax);
     return SIGMOID ? 1.0 / (1.0 + z) : z * inv;
   };
-  float* cf_lds = reinterpret_cast<float*>(c_lds);
+  aliased_float* cf_lds = reinterpret_cast<aliased_float*>(c_lds);  // the same memory, in fp32
   if (by_logit && !GROUPED) {
 #pragma unroll
     for (int i = 0; i < VPL; ++i) key[i] = lane + kWave * i < E ? (order_key(l[i]) & ~kPlace) | i : 0;
@@ -236,7 +240,7 @@ __device__ __forceinline__ bool route_token(const RouteScoredArgs& a, const floa
       // places past the last expert have a bias of -inf
       const float c = score(l[i]) + my.bias[i];
       key[i] = c > -__builtin_inff() ? (order_key(by_logit ? l[i] : c) & ~kPlace) | i : 0;
-      if (GROUPED) cf_lds[lane + kWave * i] = c;
+      if (GROUPED) cf_lds[lane + kWave * i] = c > -__builtin_inff() ? c : -__builtin_inff();
     }
   }
   if constexpr (GROUPED) {
@@ -245,7 +249,7 @@ __device__ __forceinline__ bool route_token(const RouteScoredArgs& a, const floa
     const int g = lane >> (6 - log_g);
     float c1 = -__builtin_inff(), c2 = c1;
     if (g < a.n_group) {
-      const float* cg = cf_lds + g * gs;
+      const aliased_float* cg = cf_lds + g * gs;
 #pragma unroll 4
       for (int j = lane & (lanes - 1); j < gs; j += lanes) {
         const float c = cg[j];

@@ -410,7 +410,8 @@ moe_status moe_add_rmsnorm(const void* x, int32_t x_dtype, const void* residual,
  * error of a few 1e-4 of their rms (measured), which an fp32 output would not show.  The order of a
  * row's sums may follow T, so its bits may change with the batch size.
  * Errors: INVALID_ARG (bad sizes, types or pointers; K % 32 != 0 with MXFP8; N odd with SwiGLU; x or
- * w not 16-byte aligned), UNSUPPORTED (K % 8 != 0; N or K > 2^20; MXFP8 with an F32 output). */
+ * w not 16-byte aligned), UNSUPPORTED (K % 8 != 0; N or K > 2^20; T > 2^26;
+ * MXFP8 with an F32 output). */
 typedef enum { MOE_ACT_NONE = 0, MOE_ACT_RELU = 1, MOE_ACT_GELU = 2 /* tanh form */, MOE_ACT_SILU = 3,
                MOE_ACT_SWIGLU = 4 } moe_act;
 moe_status moe_linear(const void* x, const uint8_t* x_scales, const void* w, const uint8_t* w_scales,

@@ -47,7 +47,7 @@ def linear(L, x=P, xs=None, w=P, ws=None, dt=2, T=4, N=64, K=64, bias=P, act=0, 
 @pytest.mark.parametrize("bad,want", [
     (dict(T=-1), -1), (dict(N=0), -1), (dict(K=0), -1), (dict(dt=1), -1), (dict(dt=4), -1), (dict(act=-1), -1),
     (dict(act=5), -1), (dict(rd=3), -1), (dict(od=3), -1), (dict(od=0), -1), (dict(act=4, N=63), -1),
-    (dict(K=60), -2), (dict(K=(1 << 20) + 8), -2), (dict(N=(1 << 20) + 1), -2),
+    (dict(K=60), -2), (dict(K=(1 << 20) + 8), -2), (dict(N=(1 << 20) + 1), -2), (dict(T=(1 << 26) + 1), -2),
     (dict(x=None), -1), (dict(w=None), -1), (dict(out=None), -1), (dict(x=P + 8), -1), (dict(w=P + 2), -1),
     (dict(out=P + 2), -1), (dict(out=P + 1, od=2), -1), (dict(r=P + 2), -1), (dict(bias=P + 2), -1),
     (dict(dt=3, xs=P, ws=P, K=72, od=2), -1),     # MXFP8: part of a block

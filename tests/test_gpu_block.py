@@ -137,7 +137,7 @@ def test_norm_rows_are_independent(L):
 
 
 def test_norm_many_rows(L):
-    """More rows than workgroups in a launch: every row is computed."""
+    """More rows than the tests of the widths have: every row is computed."""
     T, H = 70001, 64
     xv, rv, wv = norm_case(T, H, "bf16", "bf16")
     check_norm(L, xv, rv, wv, 1e-6)
@@ -248,6 +248,34 @@ def test_linear_epilogue(L, act, mx):
 def test_linear_large(L, T, N, K, mx):
     check_linear(L, T, N, K, out="bf16" if mx else "f32", mx=mx)
     check_linear(L, T, N, K, act="swiglu", bias=True, res="bf16", out="bf16", mx=mx)
+
+
+@pytest.mark.parametrize("T,N,K", [  # the kernels of moe_linear and their edges: few steps and many, ragged rows and columns
+    (5, 4096, 1032), (30, 4090, 520), (61, 4096, 200), (200, 1000, 1032), (512, 4096, 200), (500, 4090, 1032),
+    (1001, 4096, 136), (1001, 4090, 1032), (2048, 4096, 264), (4096, 4096, 72), (4001, 4090, 328)])
+def test_linear_kernels_bf16(L, T, N, K):
+    check_linear(L, T, N, K, bias=True, res="bf16", out="f32")
+    check_linear(L, T, N, K, act="swiglu", out="bf16")
+
+
+@pytest.mark.parametrize("T,N,K", [
+    (5, 4096, 2080), (30, 4090, 544), (61, 4096, 416), (200, 1000, 2080), (256, 1000, 96), (2048, 1000, 160),
+    (2047, 1001, 2080), (1001, 4096, 288), (2048, 4096, 128), (1990, 4090, 1184)])
+def test_linear_kernels_mxfp8(L, T, N, K):
+    check_linear(L, T, N, K, bias=True, res="f32", out="bf16", mx=True)
+    if N % 2 == 0:
+        check_linear(L, T, N, K, act="swiglu", out="bf16", mx=True)
+
+
+def test_linear_rows_do_not_touch_each_other(L):
+    """A NaN in a token row stays in that row, also in the rows the kernels fill up with."""
+    for T, N in ((3, 64), (20, 64), (60, 96), (100, 4096), (700, 4096)):
+        x, w = torch.randn(T, 256, device="cuda").bfloat16(), torch.randn(N, 256, device="cuda").bfloat16()
+        a = L.moe_linear(x, w, out_dtype=torch.float32)
+        x[T // 2, 17] = float("nan")
+        b = L.moe_linear(x, w, out_dtype=torch.float32)
+        keep = [t for t in range(T) if t != T // 2]
+        assert torch.equal(a[keep], b[keep]) and bool(torch.isnan(b[T // 2]).all())
 
 
 def test_linear_large_values(L):
@@ -361,6 +389,28 @@ def test_route_out_of_service(L, score):
             check_route(L, lg, 6, score=score, bias=bias, n_group=4, topk_group=2, group_top=top, renormalize=True)
         check_route(L, lg, 6, score=score, bias=bias, renormalize=True)
         check_route(L, lg, 6, score=score, bias=bias)
+
+
+def test_route_broken_bias(L):
+    """A NaN bias takes an expert out of service like one of -inf; huge biases order by themselves."""
+    lg = np.random.default_rng(18).normal(size=(30, 64)).astype(np.float32)
+    bias = np.zeros(64, np.float32)
+    bias[[3, 17, 40]] = np.nan
+    bias[[5, 60]] = 1e30
+    bias[9] = -1e30
+    for G, keep in ((1, 1), (4, 2), (8, 8)):
+        for score in ("sigmoid", "softmax"):
+            for top in (1, 2):
+                check_route(L, lg, 8, score=score, bias=bias, n_group=G, topk_group=keep, group_top=top)
+
+
+def test_route_equal_rows(L):
+    """Padding rows: every logit the same, the experts in order."""
+    for E, G, keep in ((64, 1, 1), (384, 8, 4), (1000, 10, 2)):
+        lg = np.zeros((9, E), np.float32)
+        lg[1], lg[2] = 5.0, -300.0
+        for score in ("sigmoid", "softmax"):
+            check_route(L, lg, 8, score=score, n_group=G, topk_group=keep, group_top=2, renormalize=True)
 
 
 def test_route_masked_and_broken_logits(L):
