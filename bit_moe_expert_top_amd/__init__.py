@@ -11,5 +11,6 @@ def __getattr__(name):
     if name == "ops":
         from . import _lib
 
+        globals()[name] = _lib  # found without this function from now on
         return _lib
     raise AttributeError(name)
