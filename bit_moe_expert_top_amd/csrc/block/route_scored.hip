@@ -1,5 +1,5 @@
 // Scored top-k routing: softmax or sigmoid scores over all experts, a bias for the choice,
-// group-limited selection, gates from the unbiased scores.  One wavefront per token.
+// group-limited selection, gates from the unbiased scores.  One wavefront per token, or per four.
 //   p = sigmoid(l) or softmax(l);  c = p + bias
 //   a group's score is the sum of its group_top largest c; the topk_group best groups stay
 //   the k largest c of the groups that stay (without a bias: the k largest l, the same order)
@@ -28,6 +28,7 @@ namespace {
 // LDS words that hold values of more than one type in turn
 typedef float __attribute__((may_alias)) aliased_float;
 typedef uint64_t __attribute__((may_alias)) aliased_u64;
+typedef float __attribute__((ext_vector_type(4), may_alias)) aliased_f32x4;
 
 constexpr int kRouteWaves = 4;
 constexpr uint64_t kKeyDead = 1;  // below the key of every selectable expert; 0: not available
@@ -263,7 +264,8 @@ __device__ __forceinline__ bool route_token(const RouteScoredArgs& a, const floa
       c1 = fmaxf(c1, o1);
     }
     const float total = a.group_top == 2 && c2 > -__builtin_inff() ? c1 + c2 : c1;
-    const float near = kNear * (1.0f + fabsf(total));
+    // (c2 is -inf where the sum leaves it out)
+    const float near = kNear * (1.0f + fabsf(c1) + fabsf(total - c1));
     int sure = 0, maybe = -1;  // groups that are better beyond doubt, and that may be (but for itself)
     const float hi = total + near, lo = total - near;
     for (int o = 0; o < a.n_group; ++o) {
@@ -414,12 +416,319 @@ __global__ __launch_bounds__(64 * kRouteWaves, VPL > 8 ? 3 : 4) void route_score
   }
 }
 
+// ---- four tokens to a wave, 16 lanes each, for large batches.  A reduction over 16 lanes is four DPP steps and
+// serves four tokens at once, where a whole wave for one token takes six and a broadcast.  A lane holds 8 M
+// logits, sorted in chunks of eight and merged into its kTop largest keys; what falls out is remembered by its
+// largest key.  Where one that was left may be among the k, more are taken, up to 16; where two taken are
+// close, their scores are compared again without bits dropped and each with its own error.  A token that is not
+// settled then, or whose groups are not, goes through route_token with the whole wave: that costs the wave
+// 5 to 10 us (much of it fetching code that is not in the instruction cache), so the bounds are tight here.
+template <int CTRL>
+__device__ __forceinline__ uint32_t row_dpp(uint32_t v) {
+  return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, 0xF, 0xF, false);
+}
+template <class Op>
+__device__ __forceinline__ uint32_t row_reduce(uint32_t v, Op op) {  // the result in all 16 lanes
+  v = op(v, row_dpp<0xB1>(v));   // quad_perm [1,0,3,2]
+  v = op(v, row_dpp<0x4E>(v));   // quad_perm [2,3,0,1]
+  v = op(v, row_dpp<0x141>(v));  // row_half_mirror
+  return op(v, row_dpp<0x140>(v));  // row_mirror
+}
+__device__ __forceinline__ uint32_t row_max_u32(uint32_t v) {
+  return row_reduce(v, [](uint32_t a, uint32_t b) { return max(a, b); });
+}
+__device__ __forceinline__ float row_add_f32(float v) {
+  return __uint_as_float(row_reduce(__float_as_uint(v), [](uint32_t a, uint32_t b) {
+    return __float_as_uint(__uint_as_float(a) + __uint_as_float(b));
+  }));
+}
+
+// From which batch on, one token / four tokens to a wave in us (sigmoid, 4 of 8 groups, top-8; 512: softmax, top-8):
+//   E        T = 4096      8192         16384        65536
+//   256      7.9 / 11.7    12.5 / 12.4  19.7 / 15.8  58.9 / 36.4
+//   384      9.4 / 12.4    15.0 / 13.7  23.7 / 19.3  74.7 / 47.4
+//   512      9.5 / 8.1     14.8 / 13.3  22.8 / 17.7  66.9 / 48.2
+constexpr int kRowsMinT = 8192;
+constexpr int kRowsGroups = 2048;  // workgroups of a launch at most (1024: 21.3 / 51.5 us at 128 / 384 experts, 2048: 20.1 / 47.4)
+constexpr int kTop = 6, kRowsMaxK = 16, kRowsMaxGroups = 16;
+
+template <int M, bool SIGMOID, bool GROUPED, bool BIASED>
+__global__ __launch_bounds__(64 * kRouteWaves, M > 2 ? 3 : 4) void route_rows_kernel(RouteScoredArgs a) {
+  constexpr int N = 8 * M, VPL = 2 * M;      // logits of a lane; of a lane of route_token
+  constexpr int kRow = 128 * M + 4;          // c of a token in LDS, and a pad: the tokens in different banks
+  constexpr int B = N > 16 ? 5 : N > 8 ? 4 : 3;
+  constexpr uint32_t kPlace = (1u << B) - 1;
+  constexpr uint32_t kOut = 0x007FFFFFu;     // the image of -inf
+  // Errors of an fp32 score, as in route_token but for a sum of 32 + 4 steps: sigmoid (p (1 - p) (|l| + 2) + 2 p)
+  // 2^-23 <= 2.73 2^-23, softmax p (|l - max| + 22) 2^-23, which is <= (22 p + 0.37) 2^-23 where the p in play sum
+  // to at most 1; adding the bias 2^-24 |c|.  Two scores, or two group sums, of magnitude m are off against each
+  // other by at most kExact (1 + m).  Dropping B bits lowers c by at most kDrop |c|.
+  constexpr float kExact = SIGMOID ? 1.0f / (1 << 19) : 1.0f / (1 << 18), kDrop = 1.0f / (1 << (23 - B));
+  __shared__ double lds[kRouteWaves][4 * kRow / 2];
+  __shared__ uint32_t chosen[kRouteWaves][4][16];
+  __shared__ __align__(16) float bias_lds[128 * M];  // -inf past the last expert
+  const int lane = wave_lane(), w = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+  const int q = lane >> 4, E = a.E;
+  int r = lane & 15;
+  aliased_float* c_lds = reinterpret_cast<aliased_float*>(lds[w]) + q * kRow;
+  const int log_g = GROUPED ? 32 - __builtin_clz(a.n_group - 1) : 0, gs = E / a.n_group;
+  const int lanes = 16 >> log_g, g = r >> (4 - log_g);  // lanes of a group (log_g <= 4), this lane's group
+  // logit 4 j + c of the lane is expert 64 j + 4 r + c
+  auto expert = [&](int i) { return 64 * (i >> 2) + 4 * r + (i & 3); };
+  for (int e = threadIdx.x; e < 128 * M; e += 64 * kRouteWaves) {
+    const float b = e < E ? (BIASED ? a.bias[e] : 0.f) : -__builtin_inff();
+    bias_lds[e] = b > -__builtin_inff() ? b : -__builtin_inff();  // a NaN is out of service too
+  }
+  __syncthreads();
+  uint32_t first = 0;  // the first lane of the group of experts 64 j + 4 r .. + 3, four bits each
+  const float inv_gs = (float)a.n_group / (float)E;
+#pragma unroll
+  for (int j = 0; j < 2 * M; ++j)
+    if (GROUPED && expert(4 * j) < E)  // as in route_scored_kernel
+      first |= ((uint32_t)(((float)expert(4 * j) + 0.5f) * inv_gs) << (4 - log_g)) << (4 * j);
+  const int64_t step = (int64_t)gridDim.x * (4 * kRouteWaves);
+  int64_t t0 = ((int64_t)blockIdx.x * kRouteWaves + w) * 4;
+  for (; t0 < a.T; t0 += step) {
+    asm volatile("" : "+v"(r));  // what follows from the lane is formed again per token, not held
+    const int64_t t = t0 + q;
+    const float* row = a.logits + min(t, (int64_t)a.T - 1) * E;
+    float l[N];
+#pragma unroll
+    for (int j = 0; j < 2 * M; ++j) {
+      const float4 v = *reinterpret_cast<const float4*>(row + min(64 * j + 4 * r, E - 4));
+      l[4 * j] = v.x, l[4 * j + 1] = v.y, l[4 * j + 2] = v.z, l[4 * j + 3] = v.w;
+    }
+    float finite = 0.f;  // a NaN or an infinity anywhere makes the sum of l * 0 a NaN
+#pragma unroll
+    for (int i = 0; i < N; ++i) finite = fmaf(l[i], 0.f, finite);
+    bool redo = finite != 0.f;
+    float lmax = 0.f, inv_sum = 1.f;
+    if (!SIGMOID) {
+      uint32_t m = 0;
+#pragma unroll
+      for (int i = 0; i < N; ++i) m = max(m, order_key(l[i]));
+      lmax = key_to_float(row_max_u32(m));
+      float z = 0.f;
+#pragma unroll
+      for (int i = 0; i < N; ++i) z += expert(i) < E ? __expf(l[i] - lmax) : 0.f;
+      inv_sum = 1.0f / row_add_f32(z);
+    }
+    auto score = [&](float v) {
+      return SIGMOID ? __builtin_amdgcn_rcpf(1.0f + __expf(-v)) : __expf(v - lmax) * inv_sum;
+    };
+    // no c is a NaN here, and no c is -0
+    auto image = [](float c) {
+      const uint32_t u = __float_as_uint(c);
+      return u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
+    };
+    uint32_t key[N];  // at or below kOut: out of service
+#pragma unroll
+    for (int j = 0; j < 2 * M; ++j) {
+      f32x4 c = {0.f, 0.f, 0.f, 0.f};
+      if (BIASED || GROUPED) {
+        const f32x4 b = *reinterpret_cast<const f32x4*>(bias_lds + 64 * j + 4 * r);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) c[i] = score(l[4 * j + i]) + b[i];
+      }
+      if (GROUPED) *reinterpret_cast<aliased_f32x4*>(c_lds + 64 * j + 4 * r) = c;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float by = BIASED ? c[i] : expert(4 * j + i) < E ? l[4 * j + i] + 0.f : -__builtin_inff();
+        key[4 * j + i] = (image(by) & ~kPlace) | (4 * j + i);
+      }
+    }
+    if constexpr (GROUPED) {
+      float c1 = -__builtin_inff(), c2 = c1;
+      if (g < a.n_group) {
+        const aliased_float* cg = c_lds + g * gs;
+#pragma unroll 4
+        for (int j = r & (lanes - 1); j < gs; j += lanes) {
+          const float c = cg[j];
+          c2 = __builtin_amdgcn_fmed3f(c1, c2, c);  // c1 >= c2: the second of the three
+          c1 = fmaxf(c1, c);
+        }
+      }
+      for (int off = 1; off < lanes; off <<= 1) {
+        const float o1 = __shfl_xor(c1, off), o2 = __shfl_xor(c2, off);
+        c2 = fmaxf(fmaxf(c2, o2), fminf(c1, o1));
+        c1 = fmaxf(c1, o1);
+      }
+      const float total = a.group_top == 2 && c2 > -__builtin_inff() ? c1 + c2 : c1;
+      const float near = kExact * (1.0f + fabsf(c1) + fabsf(total - c1)), hi = total + near, lo = total - near;
+      int sure = 0, maybe = -1;  // groups that are better beyond doubt, and that may be (but for itself)
+      for (int o = 0; o < a.n_group; ++o) {
+        const float other = __shfl(total, 16 * q + o * lanes);
+        sure += other > hi;
+        maybe += !(other < lo);
+      }
+      const bool in = g < a.n_group && maybe < a.topk_group;
+      redo |= !in && g < a.n_group && sure < a.topk_group;
+      const uint32_t kept = (uint32_t)(__ballot(in) >> (16 * q));
+#pragma unroll
+      for (int j = 0; j < 2 * M; ++j) {
+        const uint32_t on = (uint32_t)__builtin_amdgcn_sbfe((int)kept, first >> (4 * j) & 15, 1);  // all ones or zero
+#pragma unroll
+        for (int i = 0; i < 4; ++i) key[4 * j + i] &= on;
+      }
+    }
+    // the lane's kTop largest keys in order, and the largest of the others
+    uint32_t top[8], lost = 0;
+#pragma unroll
+    for (int m = 0; m < M; ++m) {
+      uint32_t v[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = key[8 * m + i];
+      sort_desc(v);
+      if (m == 0) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) top[i] = v[i];
+        continue;
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        lost = max(lost, min(top[i], v[7 - i]));
+        top[i] = max(top[i], v[7 - i]);
+      }
+#pragma unroll
+      for (int d = 4; d > 0; d >>= 1) {  // top is bitonic
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (!(i & d)) {
+            const uint32_t hi = max(top[i], top[i + d]), lo = min(top[i], top[i + d]);
+            top[i] = hi, top[i + d] = lo;
+          }
+      }
+    }
+    lost = max(lost, top[kTop]);
+    uint32_t mine = 0;  // lane j of the row: the j-th largest key
+    int pops = 0;
+    auto round = [&](int j, uint32_t on) {  // on: all ones, or zero in a row that takes no part
+      const uint32_t best = row_max_u32(top[0]);
+      // (masks rather than selects: those the compiler turns into indexing of the list)
+      const uint32_t pop = (top[0] == best ? 0xFFFFFFFFu : 0u) & on;
+      if (r == j) mine = (best & on) | (mine & ~on);
+#pragma unroll
+      for (int i = 0; i + 1 < kTop; ++i) top[i] = (top[i + 1] & pop) | (top[i] & ~pop);
+      top[kTop - 1] &= ~pop;
+      pops -= (int)pop;
+      if (pop) chosen[w][q][j] = (best & kPlace) | r << B;
+    };
+    for (int j = 0; j < a.k; ++j) round(j, 0xFFFFFFFFu);
+    // whether key o, at or below key m in order, may be above it
+    auto close = [&](uint32_t m, uint32_t o) {
+      if (!BIASED) return (m & ~kPlace) <= (o & ~kPlace);
+      const float c = key_to_float(m & ~kPlace);
+      return o > kOut && !(c - key_to_float(o & ~kPlace) > kDrop * fabsf(c) + kExact * (1.0f + fabsf(c)));
+    };
+    int n = a.k;  // candidates of the row
+    uint32_t rest = row_max_u32(max(top[0], lost));
+    bool refine = false;
+    for (;;) {  // more candidates, up to 16, where one that is left may be among the k
+      const bool more = row_max_u32(r == a.k - 1 && close(mine, rest) ? 1u : 0u) && n < 16;
+      if (!__ballot(more)) break;
+      refine = true;
+      round(n, more ? 0xFFFFFFFFu : 0u);
+      n += more;
+      rest = row_max_u32(max(top[0], lost));
+    }
+    redo |= r < a.k && mine <= kOut;
+    redo |= r == a.k - 1 && close(mine, rest);
+    // two lanes with the same key pop together
+    redo |= row_reduce((uint32_t)pops, [](uint32_t x, uint32_t y) { return x + y; }) != (uint32_t)n;
+    __builtin_amdgcn_wave_barrier();
+    const uint32_t pick = r < n ? chosen[w][q][r] : 0;
+    const int place = pick & kPlace;
+    int e = min(64 * (place >> 2) + 4 * (int)(pick >> B) + (place & 3), E - 1);
+    float p = 0.f, le = 0.f;
+    if (r < n) {
+      le = row[e];
+      p = score(le);
+    }
+    const uint32_t after = row_dpp<0x101>(mine);  // row_shl 1: the next lane's, read with all lanes on
+    if (refine || __ballot(r < n - 1 && close(mine, after))) {
+      // the candidates in order of their scores without bits dropped, each with its own error
+      const float c = BIASED ? p + bias_lds[e] : le;
+      float err = 0.f;
+      if (BIASED)
+        err = (SIGMOID ? p * (1.0f - p) * (fabsf(le) + 2.0f) + 2.0f * p : p * (lmax - le + 22.0f)) * 0x1p-23f +
+              fabsf(c) * 0x1p-24f + 1e-37f;
+      int rank = 0;
+      bool twin = false;
+#pragma unroll 1
+      for (int o = 0; o < 16; ++o) {
+        const float oc = __shfl(c, 16 * q + o), other = __shfl(err, 16 * q + o);
+        const int oe = __shfl(e, 16 * q + o);
+        const bool on = o < n && o != r;
+        rank += on && (oc > c || (oc == c && oe < e));
+        if (BIASED) twin |= on && !(fabsf(oc - c) > err + other);
+      }
+      redo |= r < n && twin;
+      const int to = 4 * (16 * q + (r < n ? rank : r));  // a permutation of the row
+      e = __builtin_amdgcn_ds_permute(to, e);
+      p = __uint_as_float(__builtin_amdgcn_ds_permute(to, (int)__float_as_uint(p)));
+    }
+    if (r >= a.k) p = 0.f;
+    const float sum = row_add_f32(p);
+    redo |= !(sum > 1e-30f);
+    uint64_t again = __ballot(redo);
+    again |= again >> 8, again |= again >> 4, again |= again >> 2, again |= again >> 1;
+    again &= 0x0001000100010001ull;  // one bit per token
+    if (t < a.T && r < a.k && !(again >> (16 * q) & 1)) {
+      a.ids[t * a.k + r] = e;
+      a.gates[t * a.k + r] = (a.renormalize ? p / sum : p) * a.scale;
+    }
+    if (again) {
+      int l0 = lane;
+      asm volatile("" : "+v"(l0));
+      LaneExperts<VPL> my;
+      const int lg = GROUPED ? log_g : 0;
+#pragma unroll
+      for (int i = 0; i < VPL; ++i) {
+        const int x = l0 + kWave * i;
+        my.bias[i] = bias_lds[x];
+        my.group[i] = GROUPED && x < E ? (uint32_t)(((float)x + 0.5f) * inv_gs) << (6 - lg) : 0;
+      }
+      float* l_lds = reinterpret_cast<float*>(lds[w] + 64 * VPL);
+      for (; again; again &= again - 1) {
+        const int64_t u = t0 + (__builtin_ctzll(again) >> 4);
+        if (u >= a.T) break;
+        __builtin_amdgcn_wave_barrier();
+        float lu[VPL];
+#pragma unroll
+        for (int i = 0; i < VPL; ++i) {
+          lu[i] = a.logits[u * E + min(l0 + kWave * i, E - 1)];
+          l_lds[l0 + kWave * i] = lu[i];
+        }
+        if (!route_token<VPL, SIGMOID, GROUPED>(a, lu, my, lg, u, lds[w], l_lds)) route_token64(a, l_lds, u, lds[w]);
+      }
+    }
+    __builtin_amdgcn_wave_barrier();
+  }
+}
+
 template <int VPL, bool SIGMOID, bool GROUPED>
 hipError_t start(const RouteScoredArgs& a, hipStream_t s) {
   const int64_t want = ((int64_t)a.T + kRouteWaves - 1) / kRouteWaves;
   route_scored_kernel<VPL, SIGMOID, GROUPED>
       <<<(unsigned)(want < kRouteGroups ? want : kRouteGroups), 64 * kRouteWaves, 0, s>>>(a);
   return hipGetLastError();
+}
+
+template <int M, bool SIGMOID, bool GROUPED>
+hipError_t start_rows(const RouteScoredArgs& a, hipStream_t s) {
+  const int64_t want = ((int64_t)a.T + 4 * kRouteWaves - 1) / (4 * kRouteWaves);
+  const unsigned grid = (unsigned)(want < kRowsGroups ? want : kRowsGroups);
+  if (a.bias)
+    route_rows_kernel<M, SIGMOID, GROUPED, true><<<grid, 64 * kRouteWaves, 0, s>>>(a);
+  else
+    route_rows_kernel<M, SIGMOID, GROUPED, false><<<grid, 64 * kRouteWaves, 0, s>>>(a);
+  return hipGetLastError();
+}
+
+template <int M>
+hipError_t go_rows(const RouteScoredArgs& a, hipStream_t s) {
+  if (a.n_group > 1) return a.sigmoid ? start_rows<M, true, true>(a, s) : start_rows<M, false, true>(a, s);
+  return a.sigmoid ? start_rows<M, true, false>(a, s) : start_rows<M, false, false>(a, s);
 }
 
 template <int VPL>
@@ -431,6 +740,14 @@ hipError_t go(const RouteScoredArgs& a, hipStream_t s) {
 }  // namespace
 
 hipError_t launch_route_scored(const RouteScoredArgs& a, hipStream_t s) {
+  if (a.T >= kRowsMinT && a.E <= 512 && a.E % 4 == 0 && a.k <= kRowsMaxK && a.n_group <= kRowsMaxGroups &&
+      (a.n_group == 1 || a.E / a.n_group % 4 == 0) &&
+      reinterpret_cast<uintptr_t>(a.logits) % 16 == 0) {
+    if (a.E <= 128) return go_rows<1>(a, s);
+    if (a.E <= 256) return go_rows<2>(a, s);
+    if (a.E <= 384) return go_rows<3>(a, s);
+    return go_rows<4>(a, s);
+  }
   const int vpl = (a.E + kWave - 1) / kWave;
   if (vpl <= 1) return go<1>(a, s);
   if (vpl <= 2) return go<2>(a, s);

@@ -439,6 +439,39 @@ def test_route_masked_and_broken_logits(L):
                 np.testing.assert_allclose(gates, gw, rtol=3e-5, atol=1e-30)
 
 
+@pytest.mark.parametrize("E,k,G,keep", [
+    (4, 4, 1, 1), (64, 6, 8, 3), (100, 10, 4, 2), (128, 16, 16, 8), (160, 6, 8, 3), (256, 8, 8, 4), (260, 3, 13, 5),
+    (384, 8, 8, 4), (384, 8, 1, 1), (384, 16, 3, 1), (512, 10, 16, 3), (512, 16, 1, 1), (508, 5, 2, 1)])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_route_batches(L, E, k, G, keep, score):
+    """Batches that fill the GPU: several tokens to a wave, tokens that have to be routed again among them."""
+    r = np.random.default_rng([E, k, G, 3])
+    T = 8197
+    lg = (r.normal(size=(T, E)) * 2).astype(np.float32)
+    lg[::7] = np.round(lg[::7])                       # ties
+    lg[5::50, : E // 2] = lg[5::50, E // 2 : E // 2 * 2]
+    lg[11::97] = 0.0
+    lg[13::97, : max(1, E // 3)] = -np.inf
+    lg[17::97] = -200.0
+    lg[T - 2] = np.round(lg[T - 2])
+    bias = (r.normal(size=E) * 0.1).astype(np.float32)
+    bias[r.permutation(E)[: E // 8]] = -np.inf
+    some = np.r_[np.arange(0, 260), np.arange(T - 60, T), np.arange(260, T, 29)]
+    for top, b, renorm in ((1, None, True), (2, bias, True), (1, bias, False), (2, None, False)):
+        kw = dict(score=score, n_group=G, topk_group=keep, group_top=top, renormalize=renorm, scale=1.5)
+        ids, gates = L.moe_route_scored(cuda(lg), k, bias=None if b is None else cuda(b), **kw)
+        ids, gates = host(ids), host(gates)
+        want, gw = OB.route_scored(lg[some], k, bias=b, **kw)
+        np.testing.assert_array_equal(ids[some], want)
+        spread = np.abs(np.where(np.isfinite(lg[some]), lg[some], 0)).max(axis=1, keepdims=True) * 2
+        np.testing.assert_array_less(np.abs(gates[some] - gw), np.abs(gw) * (spread + 16) * 2.0**-23 + 1e-38)
+        # the other tokens by the small batches' kernel
+        for t in range(0, T, 500):
+            i2, g2 = L.moe_route_scored(cuda(lg[t:t + 500]), k, bias=None if b is None else cuda(b), **kw)
+            np.testing.assert_array_equal(host(i2), ids[t:t + 500])
+            np.testing.assert_allclose(host(g2), gates[t:t + 500], rtol=1e-4, atol=1e-38)
+
+
 def test_route_long(L):
     lg = np.random.default_rng(15).normal(size=(3001, 384)).astype(np.float32)
     bias = (np.random.default_rng(16).normal(size=384) * 0.05).astype(np.float32)
