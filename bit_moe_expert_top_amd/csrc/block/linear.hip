@@ -23,25 +23,26 @@ namespace bitmoe {
 namespace {
 
 constexpr int kXcds = 8;
-template <bool MX, bool GATED, int BM, int BN, int WM, int WN, int WK, int S, int OCC, int kRow, int kSpread>
+constexpr int kRow = 128;                          // bytes of a row in a stage
+constexpr int kRows = 1024 / kRow, kChunks = kRow / 16;  // rows of a load, 16-byte chunks of a row
+template <bool MX, bool GATED, int BM, int BN, int WM, int WN, int WK, int S, int OCC, int kSpread>
 __global__ __launch_bounds__(64 * WM * WN * WK, OCC) void linear_tile_kernel(LinearArgs a, int m_tiles, int n_tiles) {
   constexpr int NW = WM * WN, kThreads = 64 * NW;      // of one K group
   constexpr int AT = BM / WM / 32, BT = BN / WN / 32;   // token and weight MFMA tiles of a wave
   constexpr int kEs = MX ? 1 : 2, kStepK = kRow / kEs;
   constexpr int kCh = MX ? 2 : 1;                       // 16-byte chunks of a lane per operand and sub-step
   constexpr int kSub = kRow / (32 * kCh);               // MFMA sub-steps of a step
-  constexpr int kRows = 1024 / kRow, kChunks = kRow / 16;  // rows of a load, chunks of a row
   constexpr int UA = BM / (kRows * NW), UB = BN / (kRows * NW);
   constexpr int LD = UA + UB;  // direct loads per wave and stage (the waits below count at least these)
   constexpr int kStage = (BM + BN) * kRow, kScale = MX ? BM + BN : 4;
   static_assert(LD % (kSpread * AT) == 0 || kSpread == 1, "refill parts");
-  static_assert(S >= 2 && S <= 4 && (WK == 1 || WK == 2) && (kRow == 128 || (kRow == 64 && !MX)), "ring");
-  static_assert(BM % (kRows * NW) == 0 && BN % (kRows * NW) == 0 && NW % 4 == 0 , "loads");
+  static_assert((S == 2 || S == 4) && (WK == 1 || WK == 2), "ring");
+  static_assert(BM % (kRows * NW) == 0 && BN % (kRows * NW) == 0 && NW % 4 == 0, "loads");
   // one object per stage: the compiler tracks direct loads per object, so a read of one stage does
   // not wait for another's
-  __shared__ __align__(16) uint8_t st0[WK * kStage], st1[WK * kStage], st2[S > 2 ? WK * kStage : 16],
-      st3[S > 3 ? WK * kStage : 16];
-  __shared__ uint32_t sc0[WK * kScale], sc1[WK * kScale], sc2[S > 2 ? WK * kScale : 4], sc3[S > 3 ? WK * kScale : 4];
+  __shared__ __align__(16) uint8_t st0[WK * kStage], st1[WK * kStage], st2[S == 4 ? WK * kStage : 16],
+      st3[S == 4 ? WK * kStage : 16];
+  __shared__ uint32_t sc0[WK * kScale], sc1[WK * kScale], sc2[S == 4 ? WK * kScale : 4], sc3[S == 4 ? WK * kScale : 4];
   const int tid = threadIdx.x % kThreads, lane = wave_lane();
   const int w = __builtin_amdgcn_readfirstlane(tid / kWave);
   const int group = WK == 1 ? 0 : __builtin_amdgcn_readfirstlane(threadIdx.x / kThreads);
@@ -74,7 +75,7 @@ __global__ __launch_bounds__(64 * WM * WN * WK, OCC) void linear_tile_kernel(Lin
   const int64_t w_first = (up ? a.n_out : 0) + (int64_t)n0;
   const buf_rsrc rw = make_rsrc(a.w + w_first * kb_bytes, (uint32_t)rows_w * kb_bytes);
   const int prow = lane / kChunks;
-  auto swizzle = [](int row) { return kRow == 128 ? row >> 1 & 7 : row >> 2 & 3; };
+  auto swizzle = [](int row) { return row >> 1 & 7; };
   const uint32_t chunk = 16u * (uint32_t)(lane % kChunks ^ swizzle(kRows * w + prow));
   uint32_t xoff[UA], woff[UB];
 #pragma unroll
@@ -146,7 +147,8 @@ __global__ __launch_bounds__(64 * WM * WN * WK, OCC) void linear_tile_kernel(Lin
       if (i < n) load_one(d, kb, i, in);
   };
 
-  // a lane's chunk offsets: the swizzle has a period of 16 rows, so it is the same for every tile.  Sub-step j: bf16 chunk 2 j + hl; MXFP8 chunks 4 j + hl and 4 j + 2 + hl.
+  // a lane's chunk offsets: the swizzle has a period of 16 rows, so it is the same for every tile.
+  // Sub-step j: bf16 chunk 2 j + hl; MXFP8 chunks 4 j + hl and 4 j + 2 + hl.
   uint32_t cofs[kChunks / 2];
 #pragma unroll
   for (int j = 0; j < kChunks / 2; ++j) cofs[j] = 16u * (uint32_t)((2 * j + hl) ^ swizzle(r32));
@@ -294,18 +296,20 @@ __global__ __launch_bounds__(64 * WM * WN * WK, OCC) void linear_tile_kernel(Lin
   for (; kb + 2 * S < nk; kb += S) {
     step(I0{}, std::true_type{}, kb);
     step(I1{}, std::true_type{}, kb + 1);
-    if constexpr (S > 2) step(I2{}, std::true_type{}, kb + 2);
-    if constexpr (S > 3) step(I3{}, std::true_type{}, kb + 3);
+    if constexpr (S == 4) {
+      step(I2{}, std::true_type{}, kb + 2);
+      step(I3{}, std::true_type{}, kb + 3);
+    }
   }
   // at most 2 S steps are left
 #pragma unroll
   for (int i = 0; i < 2; ++i, kb += S) {
     if (kb < nk) step(I0{}, std::false_type{}, kb);
     if (kb + 1 < nk) step(I1{}, std::false_type{}, kb + 1);
-    if constexpr (S > 2)
+    if constexpr (S == 4) {
       if (kb + 2 < nk) step(I2{}, std::false_type{}, kb + 2);
-    if constexpr (S > 3)
       if (kb + 3 < nk) step(I3{}, std::false_type{}, kb + 3);
+    }
   }
 
   if constexpr (WK == 2) {
@@ -394,11 +398,11 @@ __global__ __launch_bounds__(64 * WM * WN * WK, OCC) void linear_tile_kernel(Lin
   }
 }
 
-template <bool MX, bool GATED, int BM, int BN, int WM, int WN, int WK, int S, int OCC, int kRow, int kSpread>
+template <bool MX, bool GATED, int BM, int BN, int WM, int WN, int WK, int S, int OCC, int kSpread>
 hipError_t go_tile(const LinearArgs& a, hipStream_t s) {
   const int64_t m_tiles = ((int64_t)a.T + BM - 1) / BM;
   const int bn = GATED ? BN / 2 : BN, n_tiles = (a.n_out + bn - 1) / bn;
-  linear_tile_kernel<MX, GATED, BM, BN, WM, WN, WK, S, OCC, kRow, kSpread>
+  linear_tile_kernel<MX, GATED, BM, BN, WM, WN, WK, S, OCC, kSpread>
       <<<(unsigned)(m_tiles * n_tiles), 64 * WM * WN * WK, 0, s>>>(a, (int)m_tiles, n_tiles);
   return hipGetLastError();
 }
@@ -450,13 +454,13 @@ template <bool MX, bool GATED>
 hipError_t launch(const LinearArgs& a, hipStream_t s) {
   const Variant v = choose<MX>(a);
   if (v <= kRows64) return launch_linear_rows(a, MX, v == kRows16 ? 1 : v == kRows32 ? 2 : 4, s);
-  if (v == kTile64) return go_tile<MX, GATED, 64, 64, 2, 2, 1, 4, 2, 128, 1>(a, s);
-  if (v == kTile128) return go_tile<MX, GATED, 128, 128, 2, 2, 1, 2, 2, 128, 1>(a, s);
-  if constexpr (MX) return go_tile<MX, GATED, 64, 64, 2, 2, 2, 4, 2, 128, 1>(a, s);
+  if (v == kTile64) return go_tile<MX, GATED, 64, 64, 2, 2, 1, 4, 2, 1>(a, s);
+  if (v == kTile128) return go_tile<MX, GATED, 128, 128, 2, 2, 1, 2, 2, 1>(a, s);
+  if constexpr (MX) return go_tile<MX, GATED, 64, 64, 2, 2, 2, 4, 2, 1>(a, s);
   if constexpr (!MX) {
-    if (v == kTile64x128) return go_tile<MX, GATED, 64, 128, 2, 2, 1, 4, 2, 128, 1>(a, s);
-    if (v == kTile128Deep) return go_tile<MX, GATED, 128, 128, 2, 2, 1, 4, 1, 128, 1>(a, s);
-    return go_tile<MX, GATED, 256, 256, 2, 4, 1, 2, 2, 128, 2>(a, s);
+    if (v == kTile64x128) return go_tile<MX, GATED, 64, 128, 2, 2, 1, 4, 2, 1>(a, s);
+    if (v == kTile128Deep) return go_tile<MX, GATED, 128, 128, 2, 2, 1, 4, 1, 1>(a, s);
+    return go_tile<MX, GATED, 256, 256, 2, 4, 1, 2, 2, 2>(a, s);
   }
 }
 
