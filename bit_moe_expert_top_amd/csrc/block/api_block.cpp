@@ -90,7 +90,8 @@ moe_status moe_linear(const void* x, const uint8_t* x_scales, const void* w, con
     return MOE_ERR_INVALID_ARG;
   const bool mx = dtype == MOE_DT_MXFP8, gated = act == MOE_ACT_SWIGLU;
   if ((mx && K % 32) || (gated && N % 2)) return MOE_ERR_INVALID_ARG;
-  if (K % 8 || N > kMaxLinear || K > kMaxLinear || T > kMaxLinearRows || (mx && out_dtype == MOE_DT_F32)) return MOE_ERR_UNSUPPORTED;
+  if (K % 8 || N > kMaxLinear || K > kMaxLinear || T > kMaxLinearRows || (mx && out_dtype == MOE_DT_F32))
+    return MOE_ERR_UNSUPPORTED;
   if (T == 0) return MOE_OK;
   if (!x || !w || !out || (mx && (!x_scales || !w_scales))) return MOE_ERR_INVALID_ARG;
   const size_t ob = out_dtype == MOE_DT_F32 ? 4 : 2, rb = residual_dtype == MOE_DT_F32 ? 4 : 2;

@@ -449,7 +449,8 @@ __device__ __forceinline__ float row_add_f32(float v) {
 //   384      9.4 / 12.4    15.0 / 13.7  23.7 / 19.3  74.7 / 47.4
 //   512      9.5 / 8.1     14.8 / 13.3  22.8 / 17.7  66.9 / 48.2
 constexpr int kRowsMinT = 8192;
-constexpr int kRowsGroups = 2048;  // workgroups of a launch at most (1024: 21.3 / 51.5 us at 128 / 384 experts, 2048: 20.1 / 47.4)
+// workgroups of a launch at most (65536 tokens, 128 / 384 experts: 1024 21.3 / 51.5 us, 2048 20.1 / 47.4 us)
+constexpr int kRowsGroups = 2048;
 constexpr int kTop = 6, kRowsMaxK = 16, kRowsMaxGroups = 16;
 
 template <int M, bool SIGMOID, bool GROUPED, bool BIASED>

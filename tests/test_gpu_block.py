@@ -472,6 +472,31 @@ def test_route_batches(L, E, k, G, keep, score):
             np.testing.assert_allclose(host(g2), gates[t:t + 500], rtol=1e-4, atol=1e-38)
 
 
+@pytest.mark.parametrize("E,k,G,keep", [(64, 6, 4, 2), (256, 8, 8, 4), (384, 16, 1, 1), (512, 10, 1, 1), (512, 8, 16, 5)])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_route_batches_close(L, E, k, G, keep, score):
+    """Large batches whose scores are a few fp32 steps of the logit apart, within and across groups: the order is the
+    64-bit one, wherever it is found."""
+    r = np.random.default_rng([E, k, G, 5])
+    T = 8200
+    levels = np.linspace(-1.0, 2.0, 40)
+    flat = levels[r.integers(0, 40, size=(T, E))].astype(np.float32)
+    steps = r.integers(0, 4, size=(T, E)) * 10.0 ** r.integers(-8, -3, size=(T, 1))
+    lg = (flat * (1.0 + steps)).astype(np.float32)
+    # a token in eight: one level for all its larger logits, a few steps apart
+    lg[::8] = np.minimum(lg[::8], np.float32(0.5) + r.integers(0, 6, size=lg[::8].shape).astype(np.float32) * 2.0**-24)
+    some = np.r_[np.arange(0, 300), np.arange(T - 12, T), np.arange(300, T, 37)]
+    same = np.full(E, 0.25, np.float32)                       # the scores' order is the logits'
+    mixed = (r.integers(-2, 3, size=E) * 0.03125).astype(np.float32)
+    # Sums of two scores only of the levels themselves: p(l + d) + p(l - d) is 2 p(l) to within d^2, which 64
+    # bits do not hold apart for steps as small as these.
+    for top, b, x in ((1, same, lg), (1, mixed, lg), (1, None, lg), (2, same, flat)):
+        kw = dict(score=score, n_group=G, topk_group=keep, group_top=top, renormalize=True, scale=2.5)
+        ids, _ = L.moe_route_scored(cuda(x), k, bias=None if b is None else cuda(b), **kw)
+        want, _ = OB.route_scored(x[some], k, bias=b, **kw)
+        np.testing.assert_array_equal(host(ids)[some], want)
+
+
 def test_route_long(L):
     lg = np.random.default_rng(15).normal(size=(3001, 384)).astype(np.float32)
     bias = (np.random.default_rng(16).normal(size=384) * 0.05).astype(np.float32)
