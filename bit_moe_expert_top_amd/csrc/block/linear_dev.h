@@ -47,7 +47,7 @@ template <int N>
 __device__ __forceinline__ void activate(float (&r)[N], int act) {
   if (act == kActRelu) {
 #pragma unroll
-    for (int i = 0; i < N; ++i) r[i] = fmaxf(r[i], 0.0f);
+    for (int i = 0; i < N; ++i) r[i] = r[i] < 0.0f ? 0.0f : r[i];  // a NaN stays one
   } else if (act == kActSilu) {
 #pragma unroll
     for (int i = 0; i < N; ++i) r[i] = silu_f32(r[i]);

@@ -120,9 +120,21 @@ __global__ __launch_bounds__(kNormThreads) void add_rmsnorm_kernel(NormArgs a) {
         const int shared = mx_shared_exp(m ? floor_log2_bf16(m) : 0, m == 0);
         unpack8(p, v[i]);
         if (in) {
-          *reinterpret_cast<uint2*>(a.q + t * H + c) =
-              make_uint2(e4m3x4_scaled(v[i][0], v[i][1], v[i][2], v[i][3], shared),
-                         e4m3x4_scaled(v[i][4], v[i][5], v[i][6], v[i][7], shared));
+          uint2 o = make_uint2(e4m3x4_scaled(v[i][0], v[i][1], v[i][2], v[i][3], shared),
+                               e4m3x4_scaled(v[i][4], v[i][5], v[i][6], v[i][7], shared));
+          if (m >= 0x7F80u) {  // infinities and NaN: by their bits, as quantising y does
+            o = make_uint2(0, 0);
+#pragma unroll 1
+            for (int j = 0; j < 4; ++j) {
+              const uint32_t u = j == 0 ? p.x : j == 1 ? p.y : j == 2 ? p.z : p.w;
+              const uint32_t b = bf16_to_e4m3_scaled(u & 0xFFFFu, shared) | bf16_to_e4m3_scaled(u >> 16, shared) << 8;
+              if (j < 2)
+                o.x |= b << (16 * j);
+              else
+                o.y |= b << (16 * j - 32);
+            }
+          }
+          *reinterpret_cast<uint2*>(a.q + t * H + c) = o;
           if ((g & 3) == 0) a.q_scales[t * (H / 32) + c / 32] = (uint8_t)(shared + 127);
         }
       }

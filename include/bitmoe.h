@@ -430,7 +430,7 @@ moe_status moe_linear(const void* x, const uint8_t* x_scales, const void* w, con
  * An expert whose c is -inf or NaN (a bias of -inf takes it out of service; a NaN logit) is
  * chosen only when no other is left, with gate 0, and counts nothing for its group; gates whose
  * sum is 0 are 0.  All ids lie in [0, E) whatever the logits are.
- * n_group = 1 (with topk_group = 1) is routing without groups.
+ * n_group = 1 (with topk_group = 1) is routing without groups.  The last bits of a gate may change with T.
  * Errors: INVALID_ARG as moe_route; a score or group_top that is neither; E % n_group != 0;
  * topk_group outside [1, n_group]; k > topk_group * E / n_group; scale not finite.  UNSUPPORTED:
  * n_group > 64. */

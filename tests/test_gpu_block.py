@@ -136,6 +136,19 @@ def test_norm_rows_are_independent(L):
     assert torch.equal(y0[keep], y1[keep])
 
 
+def test_norm_broken_rows_quantise_alike(L):
+    """NaN and infinities in a row: q and its scales are what moe_mxfp8_quantize makes of y."""
+    xv, _, wv = norm_case(6, 256, "f32", None)
+    xv[1, 3] = float("nan")
+    xv[2, 40] = float("inf")
+    xv[4, 200] = -float("inf")
+    y = torch.empty((6, 256), dtype=torch.int16, device="cuda")
+    q, qs = torch.empty((6, 256), dtype=torch.uint8, device="cuda"), torch.empty((6, 8), dtype=torch.uint8, device="cuda")
+    L.moe_add_rmsnorm(xv, wv, 1e-6, y=y, q=q, q_scales=qs)
+    q2, qs2 = L.moe_mxfp8_quantize(y)
+    assert torch.equal(q, q2) and torch.equal(qs, qs2)
+
+
 def test_norm_many_rows(L):
     """More rows than the tests of the widths have: every row is computed."""
     T, H = 70001, 64
@@ -276,6 +289,23 @@ def test_linear_rows_do_not_touch_each_other(L):
         b = L.moe_linear(x, w, out_dtype=torch.float32)
         keep = [t for t in range(T) if t != T // 2]
         assert torch.equal(a[keep], b[keep]) and bool(torch.isnan(b[T // 2]).all())
+
+
+@pytest.mark.parametrize("act", ["none", "relu", "gelu", "silu", "swiglu"])
+@pytest.mark.parametrize("T,N", [(3, 64), (60, 96), (300, 512)])
+def test_linear_carries_nan_and_infinities(L, act, T, N):
+    """A NaN or an infinite sum comes out as the definition has it, through every activation."""
+    r = np.random.default_rng([T, N])
+    x = cuda(r.normal(size=(T, 64)).astype(np.float32), torch.bfloat16)
+    w = cuda(np.abs(r.normal(size=(N, 64))).astype(np.float32) + 0.1, torch.bfloat16)
+    for t, v in ((0, float("nan")), (1, float("inf")), (2, -float("inf"))):
+        x[t, 5] = v
+    got = values(L.moe_linear(x, w, act=act, out_dtype=torch.float32))[:3]
+    with np.errstate(invalid="ignore", over="ignore"):
+        want = OB.linear(values(x)[:3], values(w), act_name=act)
+    np.testing.assert_array_equal(np.isnan(got), np.isnan(want))
+    np.testing.assert_array_equal(got[np.isinf(want)], want[np.isinf(want)])
+    assert np.isinf(got).sum() == np.isinf(want).sum()
 
 
 def test_linear_large_values(L):
