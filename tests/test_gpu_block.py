@@ -527,6 +527,61 @@ def test_route_batches_close(L, E, k, G, keep, score):
         np.testing.assert_array_equal(host(ids)[some], want)
 
 
+def test_route_batches_replayed_and_off_alignment(L):
+    """A large batch in a captured graph, and from logits that start at any float."""
+    r = np.random.default_rng(31)
+    T, E = 9000, 256
+    lg = np.round(r.normal(size=(T, E)) * 8).astype(np.float32) / 8
+    bias = cuda((r.normal(size=E) * 0.1).astype(np.float32))
+    kw = dict(score="sigmoid", bias=bias, n_group=8, topk_group=3, group_top=2, renormalize=True)
+    buf = torch.zeros(T * E + 1, device="cuda")
+    off = buf[1:].view(T, E)
+    off.copy_(cuda(lg))
+    on = cuda(lg)
+    i0, g0 = L.moe_route_scored(on, 8, **kw)
+    i1, g1 = L.moe_route_scored(off, 8, **kw)
+    assert torch.equal(i0, i1)
+    np.testing.assert_allclose(host(g0), host(g1), rtol=1e-5)
+    ids, gates = torch.zeros_like(i0), torch.zeros_like(g0)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        L.moe_route_scored(on, 8, topk_ids=ids, topk_w=gates, **kw)
+    for turn in range(3):
+        on.copy_(cuda(np.roll(lg, turn, axis=0)))
+        graph.replay()
+        torch.cuda.synchronize()
+        want = L.moe_route_scored(on, 8, **kw)
+        assert torch.equal(ids, want[0]) and torch.equal(gates, want[1])
+
+
+def test_offsets_past_32_bits(L):
+    """More than 2^31 elements in an array: the last rows are those of a small call."""
+    last = 40
+    x = torch.zeros((1_050_000, 2056), dtype=torch.bfloat16, device="cuda")
+    w = torch.randn(2056, device="cuda").bfloat16()
+    x[-last:] = torch.randn(last, 2056, device="cuda").bfloat16()
+    y = L.moe_add_rmsnorm(x, w, 1e-6)
+    assert torch.equal(y[-last:], L.moe_add_rmsnorm(x[-last:].clone(), w, 1e-6)) and not bool(y[:1000].view(torch.bfloat16).any())
+    del x, y
+    x = torch.zeros((530_000, 64), dtype=torch.bfloat16, device="cuda")
+    w = torch.randn(4096, 64, device="cuda").bfloat16()
+    x[-last:] = torch.randn(last, 64, device="cuda").bfloat16()
+    out = L.moe_linear(x, w)
+    small = values(L.moe_linear(x[-last:].clone(), w))
+    # sums of 64 products in two orders, each rounded to bf16
+    np.testing.assert_allclose(values(out[-last:]), small, rtol=2.0**-7, atol=64 * 2.0**-22)
+    assert not bool(out[:1000].view(torch.bfloat16).any())
+    del x, out
+    lg = torch.zeros((5_600_000, 384), device="cuda")
+    lg[-last:] = torch.randn(last, 384, device="cuda")
+    ids, gates = L.moe_route_scored(lg, 4, n_group=8, topk_group=2, renormalize=True)
+    i2, g2 = L.moe_route_scored(lg[-last:].clone(), 4, n_group=8, topk_group=2, renormalize=True)
+    assert torch.equal(ids[-last:], i2) and bool((ids[:1000] == torch.arange(4, device="cuda")).all())
+    np.testing.assert_allclose(host(gates[-last:]), host(g2), rtol=1e-5)
+    del lg
+    torch.cuda.empty_cache()
+
+
 def test_route_long(L):
     lg = np.random.default_rng(15).normal(size=(3001, 384)).astype(np.float32)
     bias = (np.random.default_rng(16).normal(size=384) * 0.05).astype(np.float32)
