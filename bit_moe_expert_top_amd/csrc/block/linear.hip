@@ -237,6 +237,22 @@ __global__ __launch_bounds__(64 * WM * WN * WK, OCC) void linear_tile_kernel(Lin
   for (int b = 0; b < BT; ++b) read_w(op[0], 0, 0, b);
 #pragma unroll
   for (int t = 0; t < AT; ++t) read_x(op[0], 0, 0, t);
+  // The epilogue takes 32 token rows of the wave at a time through the wave's part of the stages (rows of
+  // 32 BT sums and a pad of four), then four consecutive columns per lane.  The residual values of the
+  // next 32 rows are fetched before this turn's stores: out may be the residual, so a load behind a
+  // store would wait for it.
+  constexpr int kPitch = 32 * BT + 4, kCols = GATED ? 16 * BT : 32 * BT, kLanes = kCols / 4;
+  constexpr int kStep = kWave / kLanes, kStores = 32 / kStep;  // rows of a store, stores of a turn
+  const int ec = 4 * (lane % kLanes), n = n0 + kCols * wn + ec, er = lane / kLanes;
+  const int64_t row0 = t0 + 32 * AT * wm + er;  // this lane's first row
+  const int rows = n < a.n_out ? (int)max((int64_t)0, min((int64_t)32 * AT, a.T - (row0 - er))) - er : 0;
+  const int64_t at0 = row0 * a.n_out + n;
+  // MXFP8: bf16 values of the first 32 rows are fetched before the last step, which covers their latency (8192 x
+  // 4096 x 2048 112 -> 106 us, 1000 x 2048 x 1024 9.6 -> 9.2 us; fp32 values do not fit the registers of 128 x 128:
+  // 30 spill, 138 us; in bf16 it gains less than 2 %).
+  constexpr bool kEarly = MX && WK == 1;
+  const bool early = kEarly && a.residual && a.vec && !a.res_f32;
+  uint2 first[kStores];
   // Step kb, its stage in buffer D and in LDS for all waves, its first operands in op[0].  MAIN: the
   // stages it fetches exist and are not the last, so this step loads and waits without a branch.  (Branches
   // around loads and waits let the compiler think at the loop's head that a buffer may still be
@@ -244,6 +260,14 @@ __global__ __launch_bounds__(64 * WM * WN * WK, OCC) void linear_tile_kernel(Lin
   auto step = [&](auto D, auto MAIN_, int kb) {
     constexpr int d = decltype(D)::value, next = (d + 1) % S;
     constexpr bool kMain = decltype(MAIN_)::value;
+    if constexpr (kEarly && !kMain) {
+      if (early && kb + 1 == nk) {
+        const uint16_t* from = reinterpret_cast<const uint16_t*>(a.residual) + at0;
+#pragma unroll
+        for (int i = 0; i < kStores; ++i)
+          if (i * kStep < rows) first[i] = *reinterpret_cast<const uint2*>(from + (int64_t)(i * kStep) * a.n_out);
+      }
+    }
     // Sub-step j: per token tile, the reads of a share of the next sub-step's operands, then the MFMAs.
     // In the last sub-step those are the next stage's, behind the barrier, and the direct loads that
     // refill this buffer are issued between the MFMAs too.
@@ -341,16 +365,7 @@ __global__ __launch_bounds__(64 * WM * WN * WK, OCC) void linear_tile_kernel(Lin
         }
   }
 
-  // ---- epilogue: 32 token rows of the wave at a time through the wave's part of the stages (rows of
-  // 32 BT sums and a pad of four), then four consecutive columns per lane.  The residual values of the
-  // next 32 rows are fetched before this turn's stores: out may be the residual, so a load behind a
-  // store would wait for it.
-  constexpr int kPitch = 32 * BT + 4, kCols = GATED ? 16 * BT : 32 * BT, kLanes = kCols / 4;
-  constexpr int kStep = kWave / kLanes, kStores = 32 / kStep;  // rows of a store, stores of a turn
-  const int ec = 4 * (lane % kLanes), n = n0 + kCols * wn + ec, er = lane / kLanes;
-  const int64_t row0 = t0 + 32 * AT * wm + er;  // this lane's first row
-  const int rows = n < a.n_out ? (int)max((int64_t)0, min((int64_t)32 * AT, a.T - (row0 - er))) - er : 0;
-  const int64_t at0 = row0 * a.n_out + n;
+  // ---- epilogue
   const FourBias bias = load_bias4<GATED>(a, n);
   Four res[kStores];
   auto fetch = [&](int t) {
@@ -360,7 +375,12 @@ __global__ __launch_bounds__(64 * WM * WN * WK, OCC) void linear_tile_kernel(Lin
         if (32 * t + i * kStep < rows) res[i] = load_residual4(a, at0 + (int64_t)(32 * t + i * kStep) * a.n_out, n);
     }
   };
-  fetch(0);
+  if (early) {
+#pragma unroll
+    for (int i = 0; i < kStores; ++i) res[i].w[0] = first[i].x, res[i].w[1] = first[i].y;
+  } else {
+    fetch(0);
+  }
   if constexpr (WK == 1) __syncthreads();  // all waves have read the last stage
   constexpr int kFit = kStage / (32 * kPitch * 4);  // waves whose part fits one stage
   static_assert((NW + kFit - 1) / kFit <= S, "epilogue staging");
