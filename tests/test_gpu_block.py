@@ -280,6 +280,15 @@ def test_linear_kernels_mxfp8(L, T, N, K):
         check_linear(L, T, N, K, act="swiglu", out="bf16", mx=True)
 
 
+@pytest.mark.parametrize("T,N,K", [(2048, 1000, 32), (2048, 1000, 160), (2047, 1004, 2080), (1001, 4096, 288),
+                                   (2048, 4096, 128), (1990, 4090, 1184), (4090, 2048, 544), (2048, 512, 4096)])
+def test_linear_mxfp8_bf16_residual(L, T, N, K):
+    check_linear(L, T, N, K, bias=True, res="bf16", out="bf16", mx=True)
+    check_linear(L, T, N, K, act="silu", res="bf16", out="bf16", mx=True, in_place=True)
+    if N % 8 == 0:
+        check_linear(L, T, N, K, act="swiglu", res="bf16", out="bf16", mx=True, in_place=True)
+
+
 def test_linear_rows_do_not_touch_each_other(L):
     """A NaN in a token row stays in that row, also in the rows the kernels fill up with."""
     for T, N in ((3, 64), (20, 64), (60, 96), (100, 4096), (700, 4096)):
