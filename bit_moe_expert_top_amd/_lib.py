@@ -380,6 +380,13 @@ def _arg(t, dtypes, shape, dev, name: str):
                      f"{dev}, got {t.dtype} {tuple(t.shape)} on {t.device}{'' if t.is_contiguous() else ' (not contiguous)'}")
 
 
+def _sizes(fn: str, bits: int, *values):
+    """Refuses integers that do not fit the C ABI's 32 bits (ctypes would pass their low 32 bits).  bits: the
+    values' union, whose sign and upper part are 0 in every ordinary call."""
+    if bits >> 31 and not all(-(1 << 31) <= v < 1 << 31 for v in values):
+        raise ValueError(f"{fn}: sizes and counts have to be below 2^31, got {values}")
+
+
 # The current device and the handle of its current stream, without the checks and the stream object of
 # torch.cuda (0.1 us instead of 3 us a call, where a small call's kernel takes 3 us); a tensor on the GPU
 # has initialised both.
@@ -412,6 +419,7 @@ def moe_add_rmsnorm(x: torch.Tensor, weight: torch.Tensor, eps: float, residual=
         raise ValueError("x: expected a contiguous float32 or bf16 tensor [T][H]")
     shape = x.shape
     T, H = shape
+    _sizes("moe_add_rmsnorm", T | H, T, H)
     if y is None and q is None:
         y = torch.empty(shape, dtype=torch.int16, device=dev)
     if (q is None) != (q_scales is None):
@@ -440,6 +448,7 @@ def moe_linear(x: torch.Tensor, w: torch.Tensor, x_scales=None, w_scales=None, b
         raise ValueError(f"moe_linear: expected x [T][K], w [N][K] and an act of {sorted(ACTS)}")
     T, K = x.shape
     N = w.shape[0]
+    _sizes("moe_linear", T | N | K, T, N, K)
     mx = x_scales is not None
     if mx != (w_scales is not None):
         raise ValueError("x_scales and w_scales go together")
@@ -468,6 +477,7 @@ def moe_route_scored(logits: torch.Tensor, k: int, score: str = "softmax", bias=
     if logits.dim() != 2 or score not in SCORES:
         raise ValueError(f"moe_route_scored: expected logits [T][E] and a score of {sorted(SCORES)}")
     T, E = logits.shape
+    _sizes("moe_route_scored", T | E | k | n_group | topk_group | group_top, T, E, k, n_group, topk_group, group_top)
     topk_ids = torch.empty((T, k), dtype=torch.int32, device=dev) if topk_ids is None else topk_ids
     topk_w = torch.empty((T, k), dtype=torch.float32, device=dev) if topk_w is None else topk_w
     _call_on(dev, "moe_route_scored", _arg(logits, (torch.float32,), (T, E), dev, "logits"),
