@@ -488,28 +488,90 @@ def moe_route_scored(logits: torch.Tensor, k: int, score: str = "softmax", bias=
 
 
 class MoeBlock:
-    """A MoE block around one layer's routed experts: norm weight, router (weight, bias for balance and
-    the arguments of moe_route_scored) and an optional shared expert, bf16 (ws1 [2Is][H], ws2 [H][Is]) or
-    MXFP8 (ws1 and ws2 as pairs (elements, scales))."""
+    """A MoE block around one layer's routed experts: norm weight, router (weight [E][H], or fewer
+    rows where the last experts are not routed to, bias for balance and the arguments of moe_route_scored) and an optional shared expert, bf16 (ws1 [2Is][H], ws2 [H][Is]) or
+    MXFP8 (ws1 and ws2 as pairs (elements, scales)).  All on the experts' device; what does not fit them is
+    refused here, and by the next block_forward after an attribute is set."""
 
     def __init__(self, experts: DeviceWeights, k: int, norm_weight, router_weight, eps: float = 1e-6,
                  router_bias=None, route: dict | None = None, ws1=None, ws2=None):
-        if (ws1 is None) != (ws2 is None):
-            raise ValueError("ws1 and ws2 go together")
         self.experts, self.k, self.eps = experts, k, eps
         self.norm_weight, self.router_weight, self.router_bias = norm_weight, router_weight, router_bias
         self.route = dict(route or {})
         self.ws1, self.ws2 = ws1, ws2
+        _check_block(self)
+
+    def __setattr__(self, name, value):
+        object.__setattr__(self, name, value)
+        object.__setattr__(self, "checked", False)  # the check takes 11 us of a call's host time
 
 
-def block_forward(blk: MoeBlock, x: torch.Tensor, residual: torch.Tensor):
+def _require(ok: bool, name: str, expected: str):
+    if not ok:
+        raise ValueError(f"{name}: expected {expected}")
+
+
+def _route_status(E: int, k: int, score: str = "softmax", n_group: int = 1, topk_group: int = 1, group_top: int = 1,
+                  renormalize: bool = False, scale: float = 1.0, topk_ids=None, topk_w=None):
+    """The status of moe_route_scored for no tokens: its checks of these arguments alone."""
+    _sizes("moe_route_scored", E | k | n_group | topk_group | group_top, E, k, n_group, topk_group, group_top)
+    return lib.moe_route_scored(None, None, 0, E, k, SCORES[score], n_group, topk_group, group_top,
+                                1 if renormalize else 0, scale, None, None, None)
+
+
+def _check_block(blk: MoeBlock):
+    """Refuses operands that do not fit the layer: block_forward would send ids to experts that are not
+    there or read past the rows, or fail with the residual stream already updated."""
+    w = blk.experts
+    H, dev = w.H, next(iter(w.t.values())).device
+    E = blk.router_weight.shape[0]
+    _require(E <= w.E, "router_weight", f"at most a row for each of the {w.E} experts, got {E}")
+    _require(1 <= blk.k <= E, "k", f"a number of experts in [1, {E}]")
+    _arg(blk.norm_weight, _BF16, (H,), dev, "norm_weight")
+    _arg(blk.router_bias, (torch.float32,), (E,), dev, "router_bias")
+    _require(lib.moe_add_rmsnorm(None, MOE_DT_F32, None, MOE_DT_F32, None, blk.eps, 0, H, None, None, None, None,
+                                 None) == 0, "eps", "a normal positive number")
+    try:
+        status = _route_status(E, blk.k, **blk.route)
+    except (TypeError, KeyError) as error:
+        raise ValueError(f"route: expected arguments of moe_route_scored, got {blk.route}") from error
+    _require(status == 0, "route", f"arguments that moe_route_scored takes for {E} experts, got {blk.route}")
+
+    def matrix(name, m, rows, cols, mx):
+        if mx:
+            _arg(m[1], _E8M0, (rows, cols // 32), dev, f"{name} scales")
+        m = m[0] if mx else m
+        _require(_arg(m, _E4M3 if mx else _BF16, (rows, cols), dev, name) is not None, name, "a matrix")
+        _require(m.data_ptr() % 16 == 0 and cols % (32 if mx else 8) == 0, name,
+                 "16-byte aligned rows of whole MXFP8 blocks" if mx else "16-byte aligned rows")
+
+    matrix("router_weight", blk.router_weight, E, H, False)
+    _require((blk.ws1 is None) == (blk.ws2 is None), "ws1 and ws2", "both or none, they go together")
+    if blk.ws1 is not None:
+        mx = isinstance(blk.ws1, (tuple, list))
+        _require(isinstance(blk.ws2, (tuple, list)) == mx, "ws2", "the type of ws1 (bf16, or MXFP8 pairs)")
+        rows = (blk.ws1[0] if mx else blk.ws1).shape[0]
+        _require(rows % 2 == 0 and rows > 0, "ws1", "gate and up rows, [2Is][H]")
+        matrix("ws1", blk.ws1, rows, H, mx)
+        matrix("ws2", blk.ws2, H, rows // 2, mx)
+    object.__setattr__(blk, "checked", True)
+
+
+def block_forward(blk: MoeBlock, x: torch.Tensor, residual: torch.Tensor | None):
     """One MoE block of a pre-norm residual stream: x (the previous sublayer's output, fp32 or bf16) joins
-    the residual stream in place, its norm is routed and run through the experts and the shared expert.
-    Returns every intermediate; ``out`` is the block's output (fp32, or bf16 with an MXFP8 shared expert),
-    to be added to ``residual`` by the next norm."""
-    w, dev = blk.experts, x.device
-    T, H = x.shape
-    mx = isinstance(blk.ws1, tuple)
+    the residual stream in place (None: x is the stream), its norm is routed and run through the experts and the
+    shared expert.  Returns every intermediate; ``out`` is the block's output (fp32, or bf16 with an MXFP8 shared
+    expert), to be added to ``residual`` by the next norm."""
+    if not blk.checked:
+        _check_block(blk)
+    w, dev = blk.experts, next(iter(blk.experts.t.values())).device
+    H = w.H
+    _require(x.dim() == 2, "x", f"[T][{H}]")
+    T = x.shape[0]
+    _require(2 * T * H < 1 << 32 and T * blk.k < 1 << 31, "x", "fewer tokens, the experts take 2 T H < 2^32")
+    for name, t in (("x", x), ("residual", residual)):
+        _require((_arg(t, tuple(_FLOAT_DT), (T, H), dev, name) or 0) % 16 == 0, name, "16-byte alignment")
+    mx = isinstance(blk.ws1, (tuple, list))
     with torch.cuda.device(dev):
         y = torch.empty((T, H), dtype=torch.int16, device=dev)
         q = torch.empty((T, H), dtype=torch.uint8, device=dev) if mx else None
