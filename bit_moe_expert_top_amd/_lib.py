@@ -363,11 +363,11 @@ MOE_DT_F32, MOE_DT_BF16, MOE_DT_MXFP8 = 1, 2, 3
 ACTS = {"none": 0, "relu": 1, "gelu": 2, "silu": 3, "swiglu": 4}
 SCORES = {"softmax": 1, "sigmoid": 2}
 # bf16 arrays are given as bfloat16 tensors or as their bits (int16), e4m3fn elements and e8m0
-# scales as tensors of those types or as bytes
+# scales as bytes or as tensors of those types, where this torch has them
 _FLOAT_DT = {torch.float32: MOE_DT_F32, torch.bfloat16: MOE_DT_BF16, torch.int16: MOE_DT_BF16}
 _BF16 = (torch.bfloat16, torch.int16)
-_E4M3 = (torch.uint8, torch.float8_e4m3fn)
-_E8M0 = (torch.uint8, torch.float8_e8m0fnu)
+_E4M3 = tuple(getattr(torch, t) for t in ("uint8", "float8_e4m3fn") if hasattr(torch, t))
+_E8M0 = tuple(getattr(torch, t) for t in ("uint8", "float8_e8m0fnu") if hasattr(torch, t))
 
 
 def _arg(t, dtypes, shape, dev, name: str):
@@ -389,9 +389,10 @@ def _sizes(fn: str, bits: int, *values):
 
 # The current device and the handle of its current stream, without the checks and the stream object of
 # torch.cuda (0.1 us instead of 3 us a call, where a small call's kernel takes 3 us); a tensor on the GPU
-# has initialised both.
-_raw_device = torch._C._cuda_getDevice
-_raw_stream = torch._C._cuda_getCurrentRawStream
+# has initialised both.  torch.cuda's own where a torch does not have these.
+_raw_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
 def _call_on(dev, fn: str, *args):

@@ -57,3 +57,20 @@ def test_block_with_experts_that_are_not_routed_to(L):
     want = OM.combine(yp, inv, host(o["gates"]).astype(np.float64), 33, sp["k"])
     # the layer's bar for experts computed in bf16
     assert np.abs(host(o["routed"]) - want).max() <= 2e-2 * np.sqrt(np.mean(want**2))
+
+
+# ------------------------------------------------------------------ the binding
+def test_calls_with_the_public_stream_queries(L, monkeypatch):
+    """As on a torch without the private ones: the call is enqueued on the current stream."""
+    monkeypatch.setattr(L, "_raw_device", torch.cuda.current_device)
+    monkeypatch.setattr(L, "_raw_stream", lambda index: torch.cuda.current_stream(index).cuda_stream)
+    lg = torch.randn(50, 64, device="cuda")
+    want = L.moe_route_scored(lg, 4)
+    torch.cuda.synchronize()
+    ids, gates = torch.zeros_like(want[0]), torch.zeros_like(want[1])
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        L.moe_route_scored(lg, 4, topk_ids=ids, topk_w=gates)
+        got = ids.clone(), gates.clone()
+    torch.cuda.synchronize()
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
