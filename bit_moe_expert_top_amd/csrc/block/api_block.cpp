@@ -20,6 +20,10 @@ constexpr int kMaxLinearRows = 1 << 26;  // T: a launch has fewer than 2^32 thre
 inline hipStream_t as_stream(void* s) { return reinterpret_cast<hipStream_t>(s); }
 inline moe_status from_hip(hipError_t e) { return e == hipSuccess ? MOE_OK : MOE_ERR_HIP; }
 inline bool aligned(const void* p, size_t to) { return reinterpret_cast<uintptr_t>(p) % to == 0; }
+inline bool overlap(const void* a, size_t an, const void* b, size_t bn) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return x < y + bn && y < x + an;
+}
 inline bool float_dtype(int32_t d) { return d == MOE_DT_F32 || d == MOE_DT_BF16; }
 
 }  // namespace
@@ -96,6 +100,10 @@ moe_status moe_linear(const void* x, const uint8_t* x_scales, const void* w, con
   if (!x || !w || !out || (mx && (!x_scales || !w_scales))) return MOE_ERR_INVALID_ARG;
   const size_t ob = out_dtype == MOE_DT_F32 ? 4 : 2, rb = residual_dtype == MOE_DT_F32 ? 4 : 2;
   if (!aligned(x, 16) || !aligned(w, 16) || !aligned(bias, 4) || !aligned(out, ob) || !aligned(residual, rb))
+    return MOE_ERR_INVALID_ARG;
+  // a workgroup reads its residual values while others have stored theirs: only the very same values may be shared
+  const size_t outs = (size_t)T * (gated ? N / 2 : N);
+  if (residual && (residual != out || residual_dtype != out_dtype) && overlap(residual, outs * rb, out, outs * ob))
     return MOE_ERR_INVALID_ARG;
   LinearArgs a{};
   a.x = static_cast<const uint8_t*>(x);

@@ -404,7 +404,8 @@ moe_status moe_add_rmsnorm(const void* x, int32_t x_dtype, const void* residual,
  *                  others the up projection (the layout of an expert's W1), and
  *                  out = silu(gate) * up has N/2 columns; the others have N
  *   residual       [T][columns of out] of residual_dtype (F32 or BF16), or NULL
- *   out            of out_dtype (F32 or BF16); may be residual itself if the types are equal
+ *   out            of out_dtype (F32 or BF16); may be residual itself if the types are equal (any other overlap
+ *                  of the two is refused)
  * Sums are fp32 on the matrix cores; bias, activation and residual are applied in fp32 and the
  * result is rounded once.  MXFP8 products go to bf16 only: the FP8 matrix cores' sums carry an
  * error of a few 1e-4 of their rms (measured), which an fp32 output would not show.  The order of a
