@@ -433,8 +433,8 @@ moe_status moe_linear(const void* x, const uint8_t* x_scales, const void* w, con
  * sum is 0 are 0.  All ids lie in [0, E) whatever the logits are.
  * n_group = 1 (with topk_group = 1) is routing without groups.  The last bits of a gate may change with T.
  * Errors: INVALID_ARG as moe_route; a score or group_top that is neither; E % n_group != 0;
- * topk_group outside [1, n_group]; k > topk_group * E / n_group; scale not finite.  UNSUPPORTED:
- * n_group > 64. */
+ * topk_group outside [1, n_group]; k > topk_group * E / n_group; scale not finite; an array not
+ * 4-byte aligned.  UNSUPPORTED: n_group > 64. */
 typedef enum { MOE_SCORE_SOFTMAX = 1, MOE_SCORE_SIGMOID = 2 } moe_score;
 moe_status moe_route_scored(const float* logits, const float* bias, int32_t T, int32_t E, int32_t k,
                             int32_t score, int32_t n_group, int32_t topk_group, int32_t group_top,
