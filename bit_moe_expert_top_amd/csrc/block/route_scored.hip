@@ -274,7 +274,8 @@ __device__ __forceinline__ bool route_token(const RouteScoredArgs& a, const floa
       maybe += !(other < lo);
     }
     bool in = g < a.n_group && maybe < a.topk_group;
-    if (__ballot(!in && g < a.n_group && sure < a.topk_group)) {
+    // (a group whose experts are all out of service, total = -inf, needs no decision: it has no key to lose)
+    if (__ballot(!in && g < a.n_group && total > -__builtin_inff() && sure < a.topk_group)) {
       // too close: the groups' sums in 64 bits
       const double inv = sum64();
 #pragma unroll 1
@@ -563,7 +564,7 @@ __global__ __launch_bounds__(64 * kRouteWaves, M > 2 ? 3 : 4) void route_rows_ke
         maybe += !(other < lo);
       }
       const bool in = g < a.n_group && maybe < a.topk_group;
-      redo |= !in && g < a.n_group && sure < a.topk_group;
+      redo |= !in && g < a.n_group && total > -__builtin_inff() && sure < a.topk_group;  // as in route_token
       const uint32_t kept = (uint32_t)(__ballot(in) >> (16 * q));
 #pragma unroll
       for (int j = 0; j < 2 * M; ++j) {

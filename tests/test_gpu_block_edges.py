@@ -74,3 +74,82 @@ def test_calls_with_the_public_stream_queries(L, monkeypatch):
         got = ids.clone(), gates.clone()
     torch.cuda.synchronize()
     assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+# ------------------------------------------------------------------ routing
+def check_route(L, lg, k, some=None, **kw):
+    bias = kw.pop("bias", None)
+    ids, gates = L.moe_route_scored(cuda(lg), k, bias=None if bias is None else cuda(bias), **kw)
+    ids, gates = host(ids), host(gates)
+    some = np.arange(len(lg)) if some is None else some
+    want, gw = OB.route_scored(lg[some], k, bias=bias, **kw)
+    np.testing.assert_array_equal(ids[some], want)
+    # exp with an argument rounded in fp32: (|l - max| + 8) 2^-23 of the gate; sums, a quotient and a product: 16 more
+    # roundings of 2^-24
+    finite = np.where(np.isfinite(lg[some]), lg[some], 0.0)
+    spread = np.abs(finite).max(axis=1, keepdims=True) * 2
+    assert np.isfinite(gates).all()
+    np.testing.assert_array_less(np.abs(gates[some] - gw), np.abs(gw) * (spread + 16) * 2.0**-23 + 1e-38)
+    return ids
+
+
+def microseconds(call, n=10):
+    """The time of a call on the GPU: the median replay of a graph of n of them."""
+    call()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        for _ in range(n):
+            call()
+    times = []
+    for _ in range(9):
+        start, end = torch.cuda.Event(True), torch.cuda.Event(True)
+        start.record()
+        graph.replay()
+        end.record()
+        torch.cuda.synchronize()
+        times.append(start.elapsed_time(end) * 1e3 / n)
+    return sorted(times)[4]
+
+
+def route_time(L, lg, k, bias=None, **kw):
+    lg, bias = cuda(lg), None if bias is None else cuda(bias)
+    ids = torch.empty(len(lg), k, dtype=torch.int32, device="cuda")
+    gates = torch.empty(len(lg), k, device="cuda")
+    return microseconds(lambda: L.moe_route_scored(lg, k, bias=bias, topk_ids=ids, topk_w=gates, **kw))
+
+
+def rows_of(T):
+    """The rows that the oracle checks of a large batch."""
+    return np.r_[np.arange(0, min(T, 300)), np.arange(300, T, 41)]
+
+
+@pytest.mark.parametrize("T", [50, 8200])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E,G,keep,k", [(64, 8, 4, 6), (256, 8, 3, 8), (384, 4, 2, 16), (512, 16, 5, 8)])
+def test_groups_out_of_service(L, T, score, E, G, keep, k):
+    """Whole groups with a bias of -inf or NaN: one, as many as leave fewer than stay, one left, none left."""
+    r = np.random.default_rng([T, E, 51])
+    lg = (r.normal(size=(T, E)) * 2).astype(np.float32)
+    lg[::9] = np.round(lg[::9])  # ties
+    gs = E // G
+    some = rows_of(T)[::4]
+    for dead in (1, G - keep + 1, G - 1, G):
+        bias = (r.normal(size=E) * 0.1).astype(np.float32)
+        for g in r.permutation(G)[:dead]:
+            bias[g * gs:(g + 1) * gs] = -np.inf if g % 2 else np.nan
+        for top in (1, 2):
+            check_route(L, lg, k, some, score=score, bias=bias, n_group=G, topk_group=keep, group_top=top, renormalize=True)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_time_with_a_group_out_of_service(L, score):
+    """A group out of service leaves the others' choice to fp32: the call takes no more than twice its time."""
+    r = np.random.default_rng(52)
+    lg = r.normal(size=(32768, 384)).astype(np.float32)
+    bias = (r.normal(size=384) * 0.05).astype(np.float32)
+    dead = bias.copy()
+    dead[48:96] = -np.inf
+    kw = dict(score=score, n_group=8, topk_group=4, group_top=2, renormalize=True)
+    plain, less = route_time(L, lg, 8, bias, **kw), route_time(L, lg, 8, dead, **kw)
+    assert less < 2 * plain, (plain, less)
