@@ -15,8 +15,9 @@
 //   c, the low bits replaced by the key's place in the lane) and k + 1 rounds of a wave maximum (six
 //   DPP steps) each pop the head of one lane's list: about 20 instructions a round.  The group sums
 //   come from c in LDS, 64 / G lanes to a group.
-// What is left (logits that are not finite, experts out of service among the chosen, more than 64
-// candidates that 64 bits would have to rank) is routed plainly in 64 bits.
+// What is left (a NaN or +inf among the logits, rows of -inf alone, experts out of service among the chosen, more
+// than 64 candidates that 64 bits would have to rank) is routed plainly in 64 bits.  A logit of -inf, a mask's
+// value, has p = 0 exactly and stays in fp32.
 #include "../common.h"
 #include "../route_dev.h"
 #include "block_kernels.h"
@@ -155,6 +156,15 @@ __device__ __forceinline__ float wave_add_f32(float v) {
   }));
 }
 
+// The largest logit of a lane, a NaN if there is one: v_maximum3_f32, two logits an instruction.
+template <int N>
+__device__ __forceinline__ float largest(const float (&l)[N]) {
+  float m = l[0];
+#pragma unroll
+  for (int i = 1; i < N; ++i) m = __builtin_elementwise_maximum(m, l[i]);
+  return m;
+}
+
 // Sorts in descending order by Batcher's merge exchange (Knuth, algorithm 5.2.2M), all indexes
 // constants after unrolling.
 template <int N>
@@ -199,15 +209,11 @@ __device__ __forceinline__ bool route_token(const RouteScoredArgs& a, const floa
   uint32_t key[VPL];
   float lmax = 0.f, inv_sum = 1.f;
   {
-    float largest = 0.f;  // a NaN or an infinity anywhere makes the sum of l - l a NaN
-#pragma unroll
-    for (int i = 0; i < VPL; ++i) largest += l[i] - l[i];
-    if (__ballot(largest != 0.f)) return false;
+    const float m = largest(l);
+    if (__ballot(!(m < __builtin_inff()))) return false;
     if (!SIGMOID) {
-      uint32_t m = 0;
-#pragma unroll
-      for (int i = 0; i < VPL; ++i) m = max(m, order_key(l[i]));
-      lmax = key_to_float(wave_max_u32(m));
+      lmax = key_to_float(wave_max_u32(order_key(m)));
+      if (lmax == -__builtin_inff()) return false;
       float z = 0.f;
 #pragma unroll
       for (int i = 0; i < VPL; ++i) z += lane + kWave * i < E ? __expf(l[i] - lmax) : 0.f;
@@ -500,16 +506,12 @@ __global__ __launch_bounds__(64 * kRouteWaves, M > 2 ? 3 : 4) void route_rows_ke
       const float4 v = *reinterpret_cast<const float4*>(row + min(64 * j + 4 * r, E - 4));
       l[4 * j] = v.x, l[4 * j + 1] = v.y, l[4 * j + 2] = v.z, l[4 * j + 3] = v.w;
     }
-    float finite = 0.f;  // a NaN or an infinity anywhere makes the sum of l * 0 a NaN
-#pragma unroll
-    for (int i = 0; i < N; ++i) finite = fmaf(l[i], 0.f, finite);
-    bool redo = finite != 0.f;
+    const float m = largest(l);
+    bool redo = !(m < __builtin_inff());
     float lmax = 0.f, inv_sum = 1.f;
     if (!SIGMOID) {
-      uint32_t m = 0;
-#pragma unroll
-      for (int i = 0; i < N; ++i) m = max(m, order_key(l[i]));
-      lmax = key_to_float(row_max_u32(m));
+      lmax = key_to_float(row_max_u32(order_key(m)));
+      redo |= lmax == -__builtin_inff();
       float z = 0.f;
 #pragma unroll
       for (int i = 0; i < N; ++i) z += expert(i) < E ? __expf(l[i] - lmax) : 0.f;
@@ -518,7 +520,7 @@ __global__ __launch_bounds__(64 * kRouteWaves, M > 2 ? 3 : 4) void route_rows_ke
     auto score = [&](float v) {
       return SIGMOID ? __builtin_amdgcn_rcpf(1.0f + __expf(-v)) : __expf(v - lmax) * inv_sum;
     };
-    // no c is a NaN here, and no c is -0
+    // (of a row that is not done again: no c is a NaN, and no c is -0)
     auto image = [](float c) {
       const uint32_t u = __float_as_uint(c);
       return u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
@@ -651,9 +653,11 @@ __global__ __launch_bounds__(64 * kRouteWaves, M > 2 ? 3 : 4) void route_rows_ke
       // the candidates in order of their scores without bits dropped, each with its own error
       const float c = BIASED ? p + bias_lds[e] : le;
       float err = 0.f;
-      if (BIASED)
-        err = (SIGMOID ? p * (1.0f - p) * (fabsf(le) + 2.0f) + 2.0f * p : p * (lmax - le + 22.0f)) * 0x1p-23f +
-              fabsf(c) * 0x1p-24f + 1e-37f;
+      if (BIASED) {
+        // (p = 0 where le is -inf)
+        err = p > 0.f ? SIGMOID ? p * (1.0f - p) * (fabsf(le) + 2.0f) + 2.0f * p : p * (lmax - le + 22.0f) : 0.f;
+        err = err * 0x1p-23f + fabsf(c) * 0x1p-24f + 1e-37f;
+      }
       int rank = 0;
       bool twin = false;
 #pragma unroll 1

@@ -153,3 +153,55 @@ def test_time_with_a_group_out_of_service(L, score):
     kw = dict(score=score, n_group=8, topk_group=4, group_top=2, renormalize=True)
     plain, less = route_time(L, lg, 8, bias, **kw), route_time(L, lg, 8, dead, **kw)
     assert less < 2 * plain, (plain, less)
+
+
+def masked_logits(T, E, G, seed):
+    """Masks of -inf: a quarter of the logits, one expert, all but a few, all but one group, all; some rows
+    without one, and ties among what is left."""
+    r = np.random.default_rng([T, E, seed])
+    lg = (r.normal(size=(T, E)) * 2).astype(np.float32)
+    lg[::5] = np.round(lg[::5])
+    gs = E // G
+    for t in range(T):
+        kind = t % 16
+        if kind < 8:
+            lg[t, r.random(E) < 0.25] = -np.inf
+        elif kind == 8:
+            lg[t, r.integers(E)] = -np.inf
+        elif kind == 9:
+            lg[t, r.permutation(E)[int(r.integers(1, 20)):]] = -np.inf
+        elif kind == 10:
+            g = int(r.integers(G))
+            lg[t, :g * gs] = lg[t, (g + 1) * gs:] = -np.inf
+        elif kind == 11:
+            lg[t, r.permutation(E)[1:]] = -np.inf
+        elif kind == 12:
+            lg[t] = -np.inf
+    return lg
+
+
+@pytest.mark.parametrize("T", [61, 8200])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E,G,keep,k", [(64, 8, 4, 6), (256, 1, 1, 8), (384, 8, 3, 16), (510, 1, 1, 10), (512, 16, 5, 8)])
+def test_masked_logits(L, T, score, E, G, keep, k):
+    lg = masked_logits(T, E, G, 53)
+    r = np.random.default_rng([E, 54])
+    bias = (r.normal(size=E) * 0.1).astype(np.float32)
+    level = np.full(E, 0.25, np.float32)  # masked experts tie with one another
+    some = rows_of(T)
+    for b, top, renorm in ((None, 1, True), (bias, 2, True), (level, 1, False), (None, 2, False)):
+        check_route(L, lg, k, some, score=score, bias=b, n_group=G, topk_group=keep, group_top=top, renormalize=renorm)
+
+
+@pytest.mark.parametrize("score,groups,biased", [("softmax", (1, 1), False), ("sigmoid", (8, 4), True)])
+def test_time_of_masked_logits(L, score, groups, biased):
+    """A quarter of each row masked: no more than twice the time of the rows without the mask."""
+    r = np.random.default_rng(55)
+    lg = r.normal(size=(32768, 384)).astype(np.float32)
+    bias = (r.normal(size=384) * 0.05).astype(np.float32) if biased else None
+    masked = np.where(r.random(lg.shape) < 0.25, np.float32(-np.inf), lg)
+    kw = dict(score=score, n_group=groups[0], topk_group=groups[1], renormalize=True)
+    plain, less = route_time(L, lg, 8, bias, **kw), route_time(L, masked, 8, bias, **kw)
+    assert less < 2 * plain, (plain, less)
+    small, few = route_time(L, lg[:64], 8, bias, **kw), route_time(L, masked[:64], 8, bias, **kw)
+    assert few < 2 * small, (small, few)
