@@ -15,9 +15,10 @@
 //   c, the low bits replaced by the key's place in the lane) and k + 1 rounds of a wave maximum (six
 //   DPP steps) each pop the head of one lane's list: about 20 instructions a round.  The group sums
 //   come from c in LDS, 64 / G lanes to a group.
-// What is left (a NaN or +inf among the logits, rows of -inf alone, experts out of service among the chosen, more
-// than 64 candidates that 64 bits would have to rank) is routed plainly in 64 bits.  A logit of -inf, a mask's
-// value, has p = 0 exactly and stays in fp32.
+// Rows of equal logits without a bias or with equal ones (padding, or a mask that leaves nothing) tie everywhere:
+// they get the first k experts.  What is left (a NaN or +inf among the logits, experts out of service among the
+// chosen, more than 64 candidates that 64 bits would have to rank) is routed plainly in 64 bits.  A logit of
+// -inf, a mask's value, has p = 0 exactly and stays in fp32.
 #include "../common.h"
 #include "../route_dev.h"
 #include "block_kernels.h"
@@ -198,6 +199,19 @@ struct LaneExperts {
   uint32_t group[VPL];  // the first of the group's lanes (see below); 0 for places past the last expert
 };
 
+// Whether all experts have the same logit and the same bias: then all scores and all groups tie, and the first k
+// experts are chosen (the first topk_group groups' are the first ones).
+__device__ __forceinline__ bool equal_row(const RouteScoredArgs& a, const float* l_lds) {
+  const int lane = wave_lane();
+  const float l0 = l_lds[0];
+  if (__ballot(l_lds[lane] != l0)) return false;  // (past the last expert its logit is repeated)
+  const float b0 = a.bias ? a.bias[0] : 0.f;
+  bool same = b0 > -__builtin_inff();
+#pragma unroll 1
+  for (int e = lane; e < a.E; e += kWave) same &= l_lds[e] == l0 && (!a.bias || a.bias[e] == b0);
+  return !__ballot(!same);
+}
+
 template <int VPL, bool SIGMOID, bool GROUPED>
 __device__ __forceinline__ bool route_token(const RouteScoredArgs& a, const float (&l)[VPL], const LaneExperts<VPL>& my,
                                             int log_g, int64_t t, double* c_lds, const float* l_lds) {
@@ -213,13 +227,18 @@ __device__ __forceinline__ bool route_token(const RouteScoredArgs& a, const floa
     if (__ballot(!(m < __builtin_inff()))) return false;
     if (!SIGMOID) {
       lmax = key_to_float(wave_max_u32(order_key(m)));
-      if (lmax == -__builtin_inff()) return false;
+      if (lmax == -__builtin_inff()) {
+        if (a.bias) return false;
+        lmax = 0.f;  // p = 0 for all
+      }
       float z = 0.f;
 #pragma unroll
       for (int i = 0; i < VPL; ++i) z += lane + kWave * i < E ? __expf(l[i] - lmax) : 0.f;
-      inv_sum = 1.0f / wave_add_f32(z);
+      z = wave_add_f32(z);
+      inv_sum = z > 0.f ? 1.0f / z : 0.f;
     }
   }
+  bool even = false;  // known as an equal row
   auto score = [&](float v) {
     return SIGMOID ? __builtin_amdgcn_rcpf(1.0f + __expf(-v)) : __expf(v - lmax) * inv_sum;
   };
@@ -281,7 +300,11 @@ __device__ __forceinline__ bool route_token(const RouteScoredArgs& a, const floa
     }
     bool in = g < a.n_group && maybe < a.topk_group;
     // (a group whose experts are all out of service, total = -inf, needs no decision: it has no key to lose)
-    if (__ballot(!in && g < a.n_group && total > -__builtin_inff() && sure < a.topk_group)) {
+    const bool close_groups = __ballot(!in && g < a.n_group && total > -__builtin_inff() && sure < a.topk_group) != 0;
+    if (close_groups) even = equal_row(a, l_lds);
+    if (even) {
+      in = g < a.topk_group;
+    } else if (close_groups) {
       // too close: the groups' sums in 64 bits
       const double inv = sum64();
 #pragma unroll 1
@@ -348,13 +371,16 @@ __device__ __forceinline__ bool route_token(const RouteScoredArgs& a, const floa
   const uint32_t below = (uint32_t)__shfl_down((int)mine, 1);
   int e = (int)(from + kWave * (mine & kPlace));
   if (close(kth, next) || __ballot(lane < a.k - 1 && close(mine, below))) {
+    const uint32_t first = (uint32_t)__builtin_amdgcn_readfirstlane((int)mine);
+    if (((first ^ next) & ~kPlace) == 0) even |= equal_row(a, l_lds);
     // too close: every expert that may be among the k is a candidate, and 64 bits rank them
-    while (close(kth, next)) {
+    while (!even && close(kth, next)) {
       if (n == kWave) return false;
       round(n++);
       next = wave_max_u32(key[0]);
     }
-    const double inv = by_logit ? 0.0 : sum64();
+    if (even) n = 0;
+    const double inv = by_logit || even ? 0.0 : sum64();
     e = (int)(from + kWave * (mine & kPlace));
     double c = -__builtin_inf();
     if (lane < n) c = by_logit ? (double)l_lds[e] : score64(l_lds[e], inv) + (double)a.bias[e];
@@ -367,12 +393,14 @@ __device__ __forceinline__ bool route_token(const RouteScoredArgs& a, const floa
     }
     // lane j takes the candidate of rank j (the ranks of the candidates are a permutation)
     e = __builtin_amdgcn_ds_permute(4 * (lane < n ? rank : lane), e);
+    if (even) e = lane;
   }
   float p = 0.f;
   if (lane < a.k) p = score(l_lds[e]);
   const float sum = wave_add_f32(p);
-  if (!(sum > 1e-30f)) return false;  // gates that fp32 does not hold
-  if (a.renormalize) p = p / sum;
+  // gates that fp32 does not hold (those of an equal row of -inf are 0)
+  if (!(sum > 1e-30f) && !(even && l_lds[0] == -__builtin_inff())) return false;
+  if (a.renormalize) p = sum > 0.f ? p / sum : 0.f;
   if (lane < a.k) {
     a.ids[t * a.k + lane] = e;
     a.gates[t * a.k + lane] = p * a.scale;

@@ -205,3 +205,52 @@ def test_time_of_masked_logits(L, score, groups, biased):
     assert less < 2 * plain, (plain, less)
     small, few = route_time(L, lg[:64], 8, bias, **kw), route_time(L, masked[:64], 8, bias, **kw)
     assert few < 2 * small, (small, few)
+
+
+@pytest.mark.parametrize("T", [70, 8200])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E,G,keep,k", [(1, 1, 1, 1), (60, 5, 2, 24), (64, 8, 8, 6), (256, 1, 1, 8), (384, 8, 4, 8),
+                                        (384, 8, 4, 16), (512, 16, 5, 8), (1000, 10, 2, 30)])
+def test_padding_rows(L, T, score, E, G, keep, k):
+    """Rows of one value (0, +-large, -inf, +inf and NaN among them) between others, rows that differ in one logit
+    only; without a bias, with equal ones, with all out of service, with one that differs."""
+    r = np.random.default_rng([T, E, k, 56])
+    lg = (r.normal(size=(T, E)) * 2).astype(np.float32)
+    for i, v in enumerate((0.0, -0.0, 3.0, -300.0, 1e30, -np.inf, np.inf, np.nan)):
+        lg[i::16] = v
+    lg[8::16] = 1.0
+    lg[8::16, E // 2] = np.nextafter(np.float32(1.0), np.float32(2.0))
+    lg[9::16] = np.where(r.random(lg[9::16].shape) < 0.5, 0.0, -0.0)
+    level = np.full(E, -0.5, np.float32)
+    odd = level.copy()
+    odd[E - 1] = 0.25
+    some = rows_of(T)[::2]
+    for b, top, renorm in ((None, 1, True), (None, 2, False), (level, 2, True), (0 * level, 1, False), (odd, 1, True),
+                           (np.full(E, -np.inf, np.float32), 2, True), (np.full(E, np.nan, np.float32), 1, True)):
+        kw = dict(score=score, n_group=G, topk_group=keep, group_top=top, renormalize=renorm, scale=1.5)
+        ids, gates = L.moe_route_scored(cuda(lg), k, bias=None if b is None else cuda(b), **kw)
+        with np.errstate(invalid="ignore"):
+            want, gw = OB.route_scored(lg[some], k, bias=b, **kw)
+        ids, gates = host(ids)[some], host(gates)[some]
+        np.testing.assert_array_equal(ids, want)
+        # the same bound as check_route's; e^-300 and its kind are 0 in fp32
+        finite = np.where(np.isfinite(lg[some]) & (np.abs(lg[some]) < 1e4), lg[some], 0.0)
+        spread = np.abs(finite).max(axis=1, keepdims=True) * 2
+        np.testing.assert_array_less(np.abs(gates - gw), np.abs(gw) * (spread + 16) * 2.0**-23 + 1e-38)
+
+
+@pytest.mark.parametrize("score,groups,biased,value", [
+    ("softmax", (1, 1), False, 0.0), ("sigmoid", (1, 1), False, 0.0), ("softmax", (8, 4), True, 0.0), ("sigmoid", (8, 4), True, 0.0),
+    ("softmax", (1, 1), False, -np.inf), ("sigmoid", (1, 1), False, -np.inf), ("sigmoid", (8, 4), True, -np.inf)])
+def test_time_of_padding_rows(L, score, groups, biased, value):
+    """Half of the batch padding, its logits all 0 or all masked, the biases (if any) not trained yet: no more than three
+    times the time of a full batch (up to 2.3 measured; 4 to 10 where such rows are routed plainly in 64 bits)."""
+    r = np.random.default_rng(57)
+    for T in (64, 32768):
+        lg = r.normal(size=(T, 384)).astype(np.float32)
+        bias = np.zeros(384, np.float32) if biased else None
+        padded = lg.copy()
+        padded[T // 2:] = value
+        kw = dict(score=score, n_group=groups[0], topk_group=groups[1], renormalize=True)
+        plain, less = route_time(L, lg, 8, bias, **kw), route_time(L, padded, 8, bias, **kw)
+        assert less < 3 * plain, (T, plain, less)
