@@ -187,11 +187,18 @@ __device__ __forceinline__ void sort_desc(uint32_t (&v)[N]) {
 }
 
 // Routes one token; false if it is one for route_token64 (nothing is written then).
-// The error of an fp32 score: exp of an argument rounded to fp32 is off by (|x| + 2) 2^-23 of its
-// value; p (1 - p) |l| <= 0.23 for the sigmoid and p |l - max| <= 0.37 for the softmax, whose sum of at
-// most 1024 terms adds (16 + 6) 2^-24, so |error of p| <= 2^-20 for both; adding the bias and dropping
-// B <= 4 bits of c adds (2^-24 + 2^(B - 23)) |c|.  Two scores compare as in 64 bits if they differ by
-// more than twice that, group sums if they differ by more than four times that: kNear covers both.
+// The errors of fp32 scores, in units u = 2^-23 and in the worst case.  exp(x) is off by (0.61 |x| + 1) u of its
+// value (the product with log2(e) and that constant's rounding, one ulp of the instruction; measured 0.61 |x| + 0.68).
+//   sigmoid: p is off by p (1 - p) (0.61 |l| + 1) + 1.5 p <= 1.9 u (measured 0.93).
+//   softmax, x = max - l (its rounding adds 0.5 x): a score's own error is p (1.11 x + 1.5) u.  The sum's is common to
+//   the token's scores: S = (additions) / 2 + 1.11 ln E + 1.5 (the terms' errors weighted by p, sum of p x <= ln E),
+//   14 additions and E <= 512: S <= 16 u, 22 and 1024: 21.3 u.  Scores that sum to at most 1 differ by at most 1, so
+//   two of them, or two sums of two (p x <= 0.72 in all), are off against each other by S + 2.3 u.
+// Adding the bias is off by |c| u / 2, dropping B <= 3 bits (4 above 512 experts) of the lower c by 8 (16) |c| u.
+// Two scores compare as in 64 bits where they differ by more than kNear (1 + |c|), 32 (64) u.  A group counts another
+// as surely better or worse if they differ by more than its own kNear (1 + |c1| + |c2|); two groups' sums are off by
+// less than the mean of their two bounds.  That is enough: of two groups in the wrong order, the one with the larger
+// bound counts the other as possible, and so every group that is as good as the other; one of them is not certain then.
 // What a lane knows of its experts lane, lane + 64, ... before it sees a token.
 template <int VPL>
 struct LaneExperts {
@@ -495,10 +502,9 @@ __global__ __launch_bounds__(64 * kRouteWaves, M > 2 ? 3 : 4) void route_rows_ke
   constexpr int B = N > 16 ? 5 : N > 8 ? 4 : 3;
   constexpr uint32_t kPlace = (1u << B) - 1;
   constexpr uint32_t kOut = 0x007FFFFFu;     // the image of -inf
-  // Errors of an fp32 score, as in route_token but for a sum of 32 + 4 steps: sigmoid (p (1 - p) (|l| + 2) + 2 p)
-  // 2^-23 <= 2.73 2^-23, softmax p (|l - max| + 22) 2^-23, which is <= (22 p + 0.37) 2^-23 where the p in play sum
-  // to at most 1; adding the bias 2^-24 |c|.  Two scores, or two group sums, of magnitude m are off against each
-  // other by at most kExact (1 + m).  Dropping B bits lowers c by at most kDrop |c|.
+  // Errors as in route_token, but for the sum's 8 M + 3 additions: S = 4 M + 3 + 1.11 ln E <= 26 u.  Two scores, or two
+  // sums of two, of magnitude m are off against each other by at most S + 2.3 u (sigmoid: 8 u) and by u m for the
+  // bias: kExact (1 + m).  Dropping B bits lowers c by at most kDrop |c|.
   constexpr float kExact = SIGMOID ? 1.0f / (1 << 19) : 1.0f / (1 << 18), kDrop = 1.0f / (1 << (23 - B));
   __shared__ double lds[kRouteWaves][4 * kRow / 2];
   __shared__ uint32_t chosen[kRouteWaves][4][16];
@@ -682,8 +688,9 @@ __global__ __launch_bounds__(64 * kRouteWaves, M > 2 ? 3 : 4) void route_rows_ke
       const float c = BIASED ? p + bias_lds[e] : le;
       float err = 0.f;
       if (BIASED) {
-        // (p = 0 where le is -inf)
-        err = p > 0.f ? SIGMOID ? p * (1.0f - p) * (fabsf(le) + 2.0f) + 2.0f * p : p * (lmax - le + 22.0f) : 0.f;
+        // S p + p (1.11 x + 1.5), as another's score may be 0 (and p = 0 where le is -inf)
+        err = SIGMOID ? p * (1.0f - p) * (fabsf(le) + 2.0f) + 2.0f * p : p * (1.25f * (lmax - le) + (4 * M + 13));
+        err = p > 0.f ? err : 0.f;
         err = err * 0x1p-23f + fabsf(c) * 0x1p-24f + 1e-37f;
       }
       int rank = 0;
