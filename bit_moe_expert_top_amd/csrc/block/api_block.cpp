@@ -69,7 +69,8 @@ moe_status moe_route_scored(const float* logits, const float* bias, int32_t T, i
   if (n_group > kMaxGroups) return MOE_ERR_UNSUPPORTED;
   if (T == 0) return MOE_OK;
   if (!logits || !topk_ids || !topk_w) return MOE_ERR_INVALID_ARG;
-  if (!aligned(logits, 4) || !aligned(bias, 4) || !aligned(topk_ids, 4) || !aligned(topk_w, 4)) return MOE_ERR_INVALID_ARG;
+  if (!aligned(logits, 4) || !aligned(bias, 4) || !aligned(topk_ids, 4) || !aligned(topk_w, 4))
+    return MOE_ERR_INVALID_ARG;
   RouteScoredArgs a{};
   a.logits = logits;
   a.bias = bias;

@@ -187,7 +187,7 @@ __global__ __launch_bounds__(64 * WM * WN * WK, OCC) void linear_tile_kernel(Lin
         acc[t][b] = mfma_bf16_32x32x16(o.w[b][0], o.x[t][0], acc[t][b]);
     }
     // The largest tile keeps its sums in the ordinary registers; there the compiler is held to issue
-    // these MFMAs here (8192 x 4096 x 4096: 212 -> 207 us).
+    // these MFMAs here (212 -> 207 us for 8192 x 4096 x 4096 with an earlier loop; 216 us with and without it now).
     if constexpr (AT * BT == 8) {
 #pragma unroll
       for (int b = 0; b < BT; ++b) hold(acc[t][b]);
@@ -248,8 +248,9 @@ __global__ __launch_bounds__(64 * WM * WN * WK, OCC) void linear_tile_kernel(Lin
   const int rows = n < a.n_out ? (int)max((int64_t)0, min((int64_t)32 * AT, a.T - (row0 - er))) - er : 0;
   const int64_t at0 = row0 * a.n_out + n;
   // MXFP8: bf16 values of the first 32 rows are fetched before the last step, which covers their latency (8192 x
-  // 4096 x 2048 112 -> 106 us, 1000 x 2048 x 1024 9.6 -> 9.2 us; fp32 values do not fit the registers of 128 x 128:
-  // 30 spill, 138 us; in bf16 it gains less than 2 %).
+  // 4096 x 2048 122 -> 108 us, 1000 x 2048 x 1024 9.7 -> 9.0 us, buffers changing from call to call).  fp32 values do
+  // not fit the registers of 128 x 128: 30 spill, and it took 138 us instead of 113 (it takes 114 now).  In bf16
+  // products it gained less than 2 %.
   constexpr bool kEarly = MX && WK == 1;
   const bool early = kEarly && a.residual && a.vec && !a.res_f32;
   uint2 first[kStores];
@@ -428,8 +429,8 @@ hipError_t go_tile(const LinearArgs& a, hipStream_t s) {
 }
 
 // Which kernel: the one whose launch takes the least time by its rounds, a round being the workgroups
-// that run at once (one or two to a CU).  The times of a round were measured at K = 4096 (us, by HIP
-// graph replays; every variant's time grows with K alike):
+// that run at once (one or two to a CU).  The times of a round were measured at K = 4096 without a residual (us, by
+// HIP graph replays):
 //   token rows x weight rows   at once    bf16    MXFP8
 //   16 x 16  (linear_rows)     256         8.2     6.1
 //   32 x 16  (linear_rows)     256         9.7     7.0
@@ -442,6 +443,11 @@ hipError_t go_tile(const LinearArgs& a, hipStream_t s) {
 //   256 x 256                  256       105      -  (does not fit the registers)
 // e.g. bf16 of 1001 x 4096: 128 x 128 with four stages 38 us, 64 x 64 55 us; 2048 x 4096: 128 x 128 67 us,
 // 64 x 128 89 us; 192 x 1024: 64 x 16 11.3 us, 64 x 64 14.5 us.
+// The rule does not look at K or the epilogue, which the launch and a tile's fill and epilogue would need for small K.
+// Against every variant, forced in turn (8 to 8192 token rows, 384 and 4096 weight rows, K = 256 to 4096, with and
+// without a residual; buffers repeated and changing): the chosen one is within 5 % of the best from K = 1024 on, but
+// for bf16 8192 x 384 x 1024 (14.6 us, 64 x 64 13.3), and up to 16 % off at K <= 512 in bf16 (8192 x 4096 x 512 with
+// an fp32 residual: 256 x 256 88 us, 128 x 128 78; 512 x 4096 x 256: 7.0 and 64 x 64 6.2).
 enum Variant { kRows16, kRows32, kRows64, kTile64, kTile64Split, kTile64x128, kTile128Deep, kTile128, kTile256 };
 template <bool MX>
 Variant choose(const LinearArgs& a) {

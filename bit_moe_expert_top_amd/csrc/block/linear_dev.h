@@ -15,7 +15,11 @@ __device__ __forceinline__ f32x16_t mfma_bf16_32x32x16(u32x4 a, u32x4 b, f32x16_
   return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0,
                                                  0, 0);
 }
-// The same with e4m3 operands of 64 k and e8m0 scales per 32 k: lane l (half h = l / 32) supplies k = 32 c + 16 h
+// The same with e4m3 operands of 64 k and e8m0 scales per 32 k.  The matrix cores' sums of these products are not fp32
+// sums: one instruction's deviates by up to 3.2e-4 of the rms of such sums (measured on random operands), more than fp32
+// rounding and less than the step of the bf16 that the result is rounded to (2^-8 of the value).  It is taken for
+// their rate: exact fp32 sums would take the bf16 instructions at half of it.
+// Lane l (half h = l / 32) supplies k = 32 c + 16 h
 // + [0, 16) in its 16-byte chunks c = 0, 1 and the scale byte of the 32-k block h.
 __device__ __forceinline__ f32x16_t mfma_mxfp8_32x32x64(u32x4 a0, u32x4 a1, u32x4 b0, u32x4 b1, f32x16_t c,
                                                         uint32_t sa, uint32_t sb) {
@@ -110,9 +114,10 @@ __device__ __forceinline__ FourBias load_bias4(const LinearArgs& a, int n) {
 }
 
 // v (and, with SwiGLU, the up columns u): the sums without bias.  Adds the bias, applies the
-// activation, adds the residual and stores, rounding once.  STREAM: non-temporal stores, for outputs
-// that are larger than the caches (8192 x 4096 bf16 of K = 4096: 221 -> 209 us, of MXFP8 K = 2048 with a
-// residual: 114 -> 100 us; non-temporal loads of the residual cost 8 us).
+// activation, adds the residual and stores, rounding once.  STREAM: non-temporal stores, for the larger tiles, whose
+// outputs are larger than the caches (with buffers that change from call to call, 8192 x 4096 in bf16, K = 4096:
+// 227 -> 220 us, SwiGLU 219 -> 216; in MXFP8, K = 2048: 106 -> 88, with a bf16 residual 112 -> 108; with the same
+// buffers each time 2 % at most).
 template <bool GATED, bool STREAM>
 __device__ __forceinline__ void epilogue4(const LinearArgs& a, int64_t at, int n, const float (&v)[4],
                                           const float (&u)[4], const FourBias& bias, const Four& res) {

@@ -11,7 +11,8 @@
 //
 // v_mfma_f32_16x16x32_bf16: lane l supplies row l % 16 and 8 k of the quarter l / 16.
 // v_mfma_scale_f32_16x16x128_f8f6f4: lane l supplies row l % 16, k = 64 c + 16 (l / 16) + [0, 16) in
-// its 16-byte chunks c = 0, 1 and the e8m0 scale of the 32-k block l / 16.
+// its 16-byte chunks c = 0, 1 and the e8m0 scale of the 32-k block l / 16.  (Its sums are not fp32 sums: see
+// mfma_mxfp8_32x32x64.)
 // Lane l receives output rows (weight rows) 4 (l / 16) + i of token column l % 16.
 #include "linear_dev.h"
 

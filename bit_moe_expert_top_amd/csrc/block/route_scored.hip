@@ -402,6 +402,8 @@ __device__ __forceinline__ bool route_token(const RouteScoredArgs& a, const floa
     e = __builtin_amdgcn_ds_permute(4 * (lane < n ? rank : lane), e);
     if (even) e = lane;
   }
+  // The gates are fp32, as those of moe_route: p's own error and a quotient, 7e-8 in the root mean square, against
+  // 2.5e-8 of 64 bits rounded once, which would take another exp in 64 bits and, for softmax, the sum's E of them.
   float p = 0.f;
   if (lane < a.k) p = score(l_lds[e]);
   const float sum = wave_add_f32(p);
@@ -485,13 +487,21 @@ __device__ __forceinline__ float row_add_f32(float v) {
   }));
 }
 
-// From which batch on, one token / four tokens to a wave in us (sigmoid, 4 of 8 groups, top-8; 512: softmax, top-8):
-//   E        T = 4096      8192         16384        65536
-//   256      7.9 / 11.7    12.5 / 12.4  19.7 / 15.8  58.9 / 36.4
-//   384      9.4 / 12.4    15.0 / 13.7  23.7 / 19.3  74.7 / 47.4
-//   512      9.5 / 8.1     14.8 / 13.3  22.8 / 17.7  66.9 / 48.2
+// From which batch on, one token / four tokens to a wave in us (top-8 with a bias; graph replays):
+//                               E     T = 4096     6144         8192         16384        65536
+//   sigmoid, 4 of 8 groups      128   7.4 / 6.8    8.8 / 10.5   10.1 / 8.6   16.7 / 12.5  51.2 / 25.6
+//                               256   8.4 / 10.3   10.0 / 12.4  12.5 / 12.2  19.1 / 14.5  59.3 / 34.4
+//                               384   8.8 / 11.7   11.7 / 13.2  13.6 / 13.4  22.7 / 18.0  73.4 / 43.9
+//                               512   9.4 / 14.2   14.5 / 15.9  15.5 / 16.2  26.4 / 23.2  83.5 / 58.1
+//   softmax                     128   6.1 / 6.0    7.2 / 8.9    8.2 / 6.4    12.8 / 10.5  38.1 / 20.4
+//                               256   6.8 / 6.4    7.8 / 10.3   9.3 / 7.0    14.2 / 9.4   44.0 / 26.6
+//                               384   7.5 / 10.1   9.3 / 8.2    11.3 / 10.5  17.2 / 12.8  50.6 / 31.2
+//                               512   8.4 / 7.5    10.6 / 12.7  12.9 / 8.8   19.9 / 16.4  60.9 / 36.8
+//   sigmoid                     384   6.4 / 6.6    8.1 / 10.4   9.8 / 10.1   15.0 / 12.7  45.2 / 30.7
+// Below 8192 the four-token kernel's time hangs on how many tokens of the batch at hand are close (a wave that has
+// one takes 3 to 5 us longer), from there on it wins or loses 1 us at most.
 constexpr int kRowsMinT = 8192;
-// workgroups of a launch at most (65536 tokens, 128 / 384 experts: 1024 21.3 / 51.5 us, 2048 20.1 / 47.4 us)
+// workgroups of a launch at most (65536 tokens, 128 / 384 experts: with 1024 it took 6 / 9 % longer)
 constexpr int kRowsGroups = 2048;
 constexpr int kTop = 6, kRowsMaxK = 16, kRowsMaxGroups = 16;
 

@@ -407,8 +407,8 @@ moe_status moe_add_rmsnorm(const void* x, int32_t x_dtype, const void* residual,
  *   out            of out_dtype (F32 or BF16); may be residual itself if the types are equal (any other overlap
  *                  of the two is refused)
  * Sums are fp32 on the matrix cores; bias, activation and residual are applied in fp32 and the
- * result is rounded once.  MXFP8 products go to bf16 only: the FP8 matrix cores' sums carry an
- * error of a few 1e-4 of their rms (measured), which an fp32 output would not show.  The order of a
+ * result is rounded once.  MXFP8 products go to bf16 only: the FP8 matrix cores' sums are not fp32 sums
+ * but carry an error of a few 1e-4 of their rms (measured), which the bits of an fp32 output would hide.  The order of a
  * row's sums may follow T, so its bits may change with the batch size.
  * Errors: INVALID_ARG (bad sizes, types or pointers; K % 32 != 0 with MXFP8; N odd with SwiGLU; x or
  * w not 16-byte aligned), UNSUPPORTED (K % 8 != 0; N or K > 2^20; T > 2^26;
@@ -431,7 +431,9 @@ moe_status moe_linear(const void* x, const uint8_t* x_scales, const void* w, con
  * An expert whose c is -inf or NaN (a bias of -inf takes it out of service; a NaN logit) is
  * chosen only when no other is left, with gate 0, and counts nothing for its group; gates whose
  * sum is 0 are 0.  All ids lie in [0, E) whatever the logits are.
- * n_group = 1 (with topk_group = 1) is routing without groups.  The last bits of a gate may change with T.
+ * n_group = 1 (with topk_group = 1) is routing without groups.  The gates are computed in fp32:
+ * with d the largest |l - max| (softmax) or |l| (sigmoid) among the chosen, a gate is off by at most (2.3 d + 30) 2^-23 of
+ * its value (about 7e-8 in the root mean square; gates below 1e-37 may be 0), and its last bits may change with T.
  * Errors: INVALID_ARG as moe_route; a score or group_top that is neither; E % n_group != 0;
  * topk_group outside [1, n_group]; k > topk_group * E / n_group; scale not finite; an array not
  * 4-byte aligned.  UNSUPPORTED: n_group > 64. */
