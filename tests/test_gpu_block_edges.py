@@ -59,6 +59,41 @@ def test_block_with_experts_that_are_not_routed_to(L):
     assert np.abs(host(o["routed"]) - want).max() <= 2e-2 * np.sqrt(np.mean(want**2))
 
 
+@pytest.mark.parametrize("mx", [False, True])
+@pytest.mark.parametrize("T", [1, 40])
+def test_block_captured_and_on_another_stream(L, T, mx):
+    """The whole block in a HIP graph, replayed on changing inputs with eager work between the replays, and on a stream of
+    its own: the bits of the eager call, the residual stream updated by each."""
+    sp, blk = tiny_block(L, mx=mx)
+    H = sp["H"]
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(T)
+    new = lambda: (torch.randn(T, H, generator=gen, device="cuda"), torch.randn(T, H, generator=gen, device="cuda").bfloat16())
+    x, res = new()
+    L.block_forward(blk, x.clone(), res.clone())
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        captured = L.block_forward(blk, x, res)
+    side = torch.cuda.Stream()
+    for _ in range(4):
+        nx, nres = new()
+        x.copy_(nx)
+        res.copy_(nres)
+        graph.replay()
+        torch.cuda.synchronize()
+        got, got_res = captured["out"].clone(), res.clone()
+        eager_res, side_res = nres.clone(), nres.clone()
+        want = L.block_forward(blk, nx, eager_res)
+        torch.cuda.synchronize()
+        with torch.cuda.stream(side):
+            beside = L.block_forward(blk, nx, side_res)
+        torch.cuda.synchronize()
+        for out, r in ((got, got_res), (beside["out"], side_res)):
+            assert torch.equal(out.view(torch.uint8), want["out"].view(torch.uint8))
+            assert torch.equal(r.view(torch.uint8), eager_res.view(torch.uint8))
+
+
 # ------------------------------------------------------------------ the binding
 def test_calls_with_the_public_stream_queries(L, monkeypatch):
     """As on a torch without the private ones: the call is enqueued on the current stream."""
@@ -254,3 +289,22 @@ def test_time_of_padding_rows(L, score, groups, biased, value):
         kw = dict(score=score, n_group=groups[0], topk_group=groups[1], renormalize=True)
         plain, less = route_time(L, lg, 8, bias, **kw), route_time(L, padded, 8, bias, **kw)
         assert less < 3 * plain, (T, plain, less)
+
+
+@pytest.mark.parametrize("T", [60, 8200])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_biases_of_very_different_size(L, T, score):
+    """Scores a few 1e-6 apart in groups whose biases are around 0, 1e3 and -1e3, 1e6: each score is rounded by its own
+    size, and the order is that of 64 bits."""
+    r = np.random.default_rng([T, 58])
+    E, G = 32, 8
+    lg = (1e-5 * r.normal(size=(T, E))).astype(np.float32)
+    bias = np.zeros(E, np.float32)
+    bias[4:8] = (1000.0, -1000.0, 0.0, 0.0)
+    bias[8:12] = (1000.0, -1000.0, -1000.0, -1000.0)
+    bias[20:24] = (1e6, -1e6, -1e6, -1e6)
+    some = rows_of(T)
+    for keep in (1, 2, 3, 5):
+        for top in (1, 2):
+            check_route(L, lg, 3, some, score=score, bias=bias, n_group=G, topk_group=keep, group_top=top, renormalize=True)
+    check_route(L, lg, 12, some, score=score, bias=bias)
