@@ -489,10 +489,11 @@ def moe_route_scored(logits: torch.Tensor, k: int, score: str = "softmax", bias=
 
 
 class MoeBlock:
-    """A MoE block around one layer's routed experts: norm weight, router (weight [E][H], or fewer
-    rows where the last experts are not routed to, bias for balance and the arguments of moe_route_scored) and an optional shared expert, bf16 (ws1 [2Is][H], ws2 [H][Is]) or
-    MXFP8 (ws1 and ws2 as pairs (elements, scales)).  All on the experts' device; what does not fit them is
-    refused here, and by the next block_forward after an attribute is set."""
+    """A MoE block around one layer's routed experts: norm weight, router (weight [E][H], or fewer rows where
+    the last experts are not routed to, bias for balance and the arguments of moe_route_scored) and an optional
+    shared expert, bf16 (ws1 [2Is][H], ws2 [H][Is]) or MXFP8 (ws1 and ws2 as pairs (elements, scales)).  All on
+    the experts' device; what does not fit them is refused here, and by the next block_forward after an
+    attribute is set."""
 
     def __init__(self, experts: DeviceWeights, k: int, norm_weight, router_weight, eps: float = 1e-6,
                  router_bias=None, route: dict | None = None, ws1=None, ws2=None):
