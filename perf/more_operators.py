@@ -304,9 +304,10 @@ def _exact_quantize(case, s):
             top = part.abs().amax(1)
             top = torch.stack([t.amax() for t in top.split(by)]) if by > 1 else top
             scales[i // by:i // by + len(top), j] = top / 448
-            # the elements are those of the scale as it is stored
-            stored = (top / 448).float().double().repeat_interleave(by)[:len(x), None]
-            v = torch.where(stored > 0, part / stored, 0.0)
+            # the block's values with the largest brought to 448 (by the unrounded scale: 3/8 of the largest lies half
+            # way between two elements)
+            top = top.repeat_interleave(by)[:len(x), None]
+            v = torch.where(top > 0, part * 448 / top, 0.0)
             # e4m3: steps of 2^-3 of the value's own power of two, of 2^-9 below 2^-6, no value above 448
             unit = torch.exp2(torch.floor(torch.log2(v.abs().clamp(min=2.0 ** -6))) - 3)
             q[i:i + step, j * BLOCK:(j + 1) * BLOCK] = (torch.round(v / unit) * unit).clamp(-448, 448)
