@@ -68,6 +68,13 @@ _SIGS = {
     "moe_add_rmsnorm": (_i32, [_p, _i32, _p, _i32, _p, ctypes.c_float, _i32, _i32, _p, _p, _p, _p, _p]),
     "moe_linear": (_i32, [_p] * 4 + [_i32] * 4 + [_p, _i32, _p, _i32, _p, _i32, _p]),
     "moe_route_scored": (_i32, [_p, _p] + [_i32] * 8 + [ctypes.c_float, _p, _p, _p]),
+    "moe_fp8_quantize": (_i32, [_p, _i32, _i64, _i32, _i32, _p, _p, _p]),
+    "moe_linear_fp8": (_i32, [_p] * 4 + [_i32] * 3 + [_p, _i32, _p, _i32, _p, _p]),
+    "moe_glu": (_i32, [_p, _p] + [_i32] * 4 + [_p, _p, _p]),
+    "moe_linear_backward_ws_bytes": (_sz, [_i32] * 3),
+    "moe_linear_backward": (_i32, [_p] * 3 + [_i32] * 3 + [_p, _i32, _p, _i32, _i32, _p, _sz, _p]),
+    "moe_glu_backward_ws_bytes": (_sz, [_i32] * 3),
+    "moe_glu_backward": (_i32, [_p] * 4 + [_i32] * 4 + [_p, _i32, _p, _i32, _i32, _p, _sz, _p]),
     "moe_status_str": (ctypes.c_char_p, [_i32]),
     "moe_tier_plan": (_i32, [ctypes.POINTER(MoeTierState), _p, _i64, _p, _p, _p]),
     "moe_tier_load": (_i32, [ctypes.POINTER(MoeWeights), ctypes.POINTER(MoeWeights), _p, _p, _i32, _p]),
@@ -467,6 +474,127 @@ def moe_linear(x: torch.Tensor, w: torch.Tensor, x_scales=None, w_scales=None, b
              MOE_DT_MXFP8 if mx else MOE_DT_BF16, T, N, K, _arg(bias, (torch.float32,), (N,), dev, "bias"), ACTS[act],
              pr, rd, _arg(out, (out.dtype,), (T, cols), dev, "out"), _FLOAT_DT[out.dtype])
     return out
+
+
+def moe_fp8_quantize(x: torch.Tensor, block_rows: int = 1, q=None, scales=None):
+    """FP8 (e4m3) elements of x [rows][K] (fp32 or bf16) and their fp32 scales max|x| / 448, one for each block of
+    block_rows (1: activations, 128: weights) x 128 values.  Returns (q, scales)."""
+    dev = x.device
+    if x.dim() != 2 or block_rows not in (1, 128) or x.dtype not in _FLOAT_DT:
+        raise ValueError("moe_fp8_quantize: expected x [rows][K], fp32 or bf16, and block_rows 1 or 128")
+    rows, K = x.shape
+    _sizes("moe_fp8_quantize", rows | K, rows, K)
+    grid = ((rows + block_rows - 1) // block_rows, (K + 127) // 128)
+    q = torch.empty((rows, K), dtype=torch.uint8, device=dev) if q is None else q
+    scales = torch.empty(grid, dtype=torch.float32, device=dev) if scales is None else scales
+    _call_on(dev, "moe_fp8_quantize", _arg(x, (x.dtype,), (rows, K), dev, "x"), _FLOAT_DT[x.dtype], rows, K, block_rows,
+             _arg(q, _E4M3, (rows, K), dev, "q"), _arg(scales, (torch.float32,), grid, dev, "scales"))
+    return q, scales
+
+
+def moe_linear_fp8(x: torch.Tensor, x_scales: torch.Tensor, w: torch.Tensor, w_scales: torch.Tensor, bias=None,
+                   act: str = "none", residual=None, out=None):
+    """out = act(x W^T + bias) + residual in bf16, x [T][K] and w [N][K] FP8 elements with fp32 scales as
+    moe_fp8_quantize makes them (block_rows 1 and 128; swiglu: gate and up quantised apart and stacked, elements and
+    scales).  The rest as moe_linear."""
+    dev = x.device
+    if x.dim() != 2 or w.dim() != 2 or act not in ACTS:
+        raise ValueError(f"moe_linear_fp8: expected x [T][K], w [N][K] and an act of {sorted(ACTS)}")
+    T, K = x.shape
+    N = w.shape[0]
+    _sizes("moe_linear_fp8", T | N | K, T, N, K)
+    gated = act == "swiglu"
+    cols, kb = (N // 2 if gated else N), (K + 127) // 128
+    blocks = (cols + 127) // 128 * (2 if gated else 1)
+    if out is None:
+        out = torch.empty((T, cols), dtype=torch.int16, device=dev)
+    pr, rd = None, MOE_DT_F32
+    if residual is not None:
+        pr, rd = _arg(residual, tuple(_FLOAT_DT), (T, cols), dev, "residual"), _FLOAT_DT[residual.dtype]
+    _call_on(dev, "moe_linear_fp8", _arg(x, _E4M3, (T, K), dev, "x"),
+             _arg(x_scales, (torch.float32,), (T, kb), dev, "x_scales"), _arg(w, _E4M3, (N, K), dev, "w"),
+             _arg(w_scales, (torch.float32,), (blocks, kb), dev, "w_scales"), T, N, K,
+             _arg(bias, (torch.float32,), (N,), dev, "bias"), ACTS[act], pr, rd, _arg(out, _BF16, (T, cols), dev, "out"))
+    return out
+
+
+def _glu_act(fn: str, act: str) -> int:
+    if act not in ACTS or act == "swiglu":
+        raise ValueError(f"{fn}: expected an act of {sorted(set(ACTS) - {'swiglu'})}, the gate's")
+    return ACTS[act]
+
+
+def moe_glu(x: torch.Tensor, w: torch.Tensor, act: str = "silu", a=None, out=None):
+    """h = act(g) * u with [g | u] = x W^T; x [T][K] and w [2I][K] bf16, the gate's rows first.  a (bf16 [T][2I]),
+    if given, receives [g | u] for moe_glu_backward.  Returns h, bf16 [T][I]."""
+    dev, code = x.device, _glu_act("moe_glu", act)
+    if x.dim() != 2 or w.dim() != 2 or w.shape[0] % 2:
+        raise ValueError("moe_glu: expected x [T][K] and w [2I][K]")
+    (T, K), I = x.shape, w.shape[0] // 2
+    _sizes("moe_glu", T | I | K, T, I, K)
+    out = torch.empty((T, I), dtype=torch.int16, device=dev) if out is None else out
+    _call_on(dev, "moe_glu", _arg(x, _BF16, (T, K), dev, "x"), _arg(w, _BF16, (2 * I, K), dev, "w"), T, I, K, code,
+             _arg(a, _BF16, (T, 2 * I), dev, "a"), _arg(out, _BF16, (T, I), dev, "out"))
+    return out
+
+
+def _grad_outputs(fn: str, T: int, N: int, K: int, dev, x, w, dx, dw, need_dx, need_dw, accumulate):
+    """The arguments of a gradient call from x to accumulate, and the outputs; those that are not needed are None."""
+    if accumulate and dw is None:
+        raise ValueError(f"{fn}: accumulate adds to a dw that is given")
+    if not need_dx and not need_dw:
+        raise ValueError(f"{fn}: expected need_dx or need_dw")
+    if dx is None and need_dx:
+        dx = torch.empty((T, K), dtype=torch.int16, device=dev)
+    if dw is None and need_dw:
+        dw = torch.empty((N, K), dtype=torch.int16, device=dev)
+    dx, dw = dx if need_dx else None, dw if need_dw else None
+    kind = lambda t: MOE_DT_BF16 if t is None else _FLOAT_DT.get(t.dtype, 0)
+    any_float = tuple(_FLOAT_DT)
+    return dx, dw, (_arg(x, _BF16, (T, K), dev, "x"), _arg(w, _BF16, (N, K), dev, "w")), (
+        _arg(dx, any_float, (T, K), dev, "dx"), kind(dx), _arg(dw, any_float, (N, K), dev, "dw"), kind(dw),
+        1 if accumulate else 0)
+
+
+def _grad_ws(ws, need: int, dev):
+    """The workspace of a gradient call, and its size in bytes."""
+    if ws is None:
+        ws = torch.empty(need, dtype=torch.uint8, device=dev)
+    _require(ws.dim() == 1, "ws", "a 1-d uint8 tensor")
+    return ws, _arg(ws, (torch.uint8,), ws.shape, dev, "ws"), ws.numel()
+
+
+def moe_linear_backward(dy: torch.Tensor, x, w, dx=None, dw=None, need_dx: bool = True, need_dw: bool = True,
+                        accumulate: bool = False, ws=None):
+    """The gradients of y = x W^T: dx = dy W [T][K] and dw = dy^T x [N][K] (added to dw with accumulate); dy [T][N], x
+    [T][K] and w [N][K] bf16, dx and dw fp32 or bf16 (bf16 where not given).  What is not needed is None, and the
+    operand that only it reads may be.  ws: moe_linear_backward_ws_bytes bytes, allocated if not given.
+    Returns (dx, dw)."""
+    dev = dy.device
+    if dy.dim() != 2 or (need_dw and x is None) or (need_dx and w is None):
+        raise ValueError("moe_linear_backward: expected dy [T][N], x for dw and w for dx")
+    (T, N), K = dy.shape, (x if w is None else w).shape[-1]
+    _sizes("moe_linear_backward", T | N | K, T, N, K)
+    dx, dw, operands, outs = _grad_outputs("moe_linear_backward", T, N, K, dev, x, w, dx, dw, need_dx, need_dw, accumulate)
+    ws, pws, n = _grad_ws(ws, lib.moe_linear_backward_ws_bytes(T, N, K), dev)
+    _call_on(dev, "moe_linear_backward", _arg(dy, _BF16, (T, N), dev, "dy"), *operands, T, N, K, *outs, pws, n)
+    return dx, dw
+
+
+def moe_glu_backward(dh: torch.Tensor, a: torch.Tensor, x, w, act: str = "silu", dx=None, dw=None, need_dx: bool = True,
+                     need_dw: bool = True, accumulate: bool = False, ws=None):
+    """The gradients of moe_glu from that of its output dh [T][I] and the pre-activations a [T][2I] it kept: dx [T][K]
+    and dw [2I][K].  The rest as moe_linear_backward.  Returns (dx, dw)."""
+    dev, code = dh.device, _glu_act("moe_glu_backward", act)
+    if dh.dim() != 2 or (need_dw and x is None) or (need_dx and w is None):
+        raise ValueError("moe_glu_backward: expected dh [T][I], x for dw and w for dx")
+    (T, I), K = dh.shape, (x if w is None else w).shape[-1]
+    _sizes("moe_glu_backward", T | I | K, T, I, K)
+    dx, dw, operands, outs = _grad_outputs("moe_glu_backward", T, 2 * I, K, dev, x, w, dx, dw, need_dx, need_dw, accumulate)
+    ws, pws, n = _grad_ws(ws, lib.moe_glu_backward_ws_bytes(T, I, K), dev)
+    _call_on(dev, "moe_glu_backward", _arg(dh, _BF16, (T, I), dev, "dh"), _arg(a, _BF16, (T, 2 * I), dev, "a"), *operands,
+             T, I, K, code, *outs, pws, n)
+    return dx, dw
 
 
 def moe_route_scored(logits: torch.Tensor, k: int, score: str = "softmax", bias=None, n_group: int = 1,

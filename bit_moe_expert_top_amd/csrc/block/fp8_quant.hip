@@ -1,0 +1,156 @@
+// Quantisation to FP8 (e4m3fn) with an fp32 scale for each block of 128 values of a row, or of 128 x 128 values:
+//   s = max|x| / 448,  q = x / s rounded to e4m3 (nearest even)
+// Both divisions are IEEE fp32.  x / s of a block costs three instructions a value: with r = 1 / s rounded,
+// q0 = x r is within an ulp, and q0 + (x - q0 s) r rounds to the correct quotient (Markstein), where nothing
+// under- or overflows; blocks outside [2^-60, 2^100] are divided plainly.  A block whose scale is 0 has elements 0.
+#include "../common.h"
+#include "block_kernels.h"
+
+namespace bitmoe {
+
+namespace {
+
+constexpr int kThreads = 256;
+
+// eight values of a row as fp32
+__device__ __forceinline__ void load8(const float* p, float (&v)[8]) {
+  const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
+  v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
+  v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+}
+__device__ __forceinline__ void load8(const uint16_t* p, float (&v)[8]) {
+  const uint4 a = *reinterpret_cast<const uint4*>(p);
+  const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    v[2 * i] = bf16_to_f32(w[i] & 0xFFFFu);
+    v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+  }
+}
+
+// The largest magnitude's bits: NaN counts as larger than infinity.
+__device__ __forceinline__ uint32_t top8(const float (&v)[8]) {
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(v[i]) & 0x7FFFFFFFu);
+  return m;
+}
+
+struct Scale {
+  float s, r;  // s = top / 448 and 1 / s
+  bool plain;  // outside the range of the short division
+};
+__device__ __forceinline__ Scale scale_of(uint32_t top) {
+  Scale c;
+  const float m = __uint_as_float(top);
+  c.s = m / 448.0f;
+  c.plain = !(m >= 0x1p-60f && m <= 0x1p100f);
+  c.r = c.plain ? 0.0f : 1.0f / c.s;
+  return c;
+}
+
+__device__ __forceinline__ uint32_t pack4(float a, float b, float c, float d) {
+  auto in = [](float v) { return __builtin_amdgcn_fmed3f(v, 448.0f, -448.0f); };
+  const int lo = __builtin_amdgcn_cvt_pk_fp8_f32(in(a), in(b), 0, false);
+  return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(in(c), in(d), lo, true);
+}
+
+__device__ __forceinline__ uint2 quantize8(const float (&v)[8], const Scale& c) {
+  float q[8];
+  if (!c.plain) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float q0 = v[i] * c.r;
+      q[i] = fmaf(fmaf(-q0, c.s, v[i]), c.r, q0);
+    }
+    return make_uint2(pack4(q[0], q[1], q[2], q[3]), pack4(q[4], q[5], q[6], q[7]));
+  }
+  uint32_t w[2] = {0, 0};
+  if (c.s == 0.0f) return make_uint2(0, 0);
+#pragma unroll 1
+  for (int h = 0; h < 2; ++h) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float x = h ? v[4 + i] : v[i];
+      const float d = x / c.s;
+      const uint32_t b = d == d ? pack4(d, 0.f, 0.f, 0.f) & 0xFFu : 0x7Fu;
+      w[h] |= b << (8 * i);
+    }
+  }
+  return make_uint2(w[0], w[1]);
+}
+
+// A scale per row and 128 values: 16 lanes to a block.
+template <typename XT>
+__global__ __launch_bounds__(kThreads) void quantize_rows_kernel(const XT* x, int64_t rows, int K, int kb, uint8_t* q,
+                                                                 float* scales) {
+  const int64_t blocks = rows * kb;
+  for (int64_t b = (int64_t)blockIdx.x * (kThreads / 16) + threadIdx.x / 16; b < blocks;
+       b += (int64_t)gridDim.x * (kThreads / 16)) {
+    const int64_t row = b / kb;
+    const int j = (int)(b - row * kb), c = 128 * j + 8 * (threadIdx.x % 16);
+    float v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+    if (c < K) load8(x + row * K + c, v);
+    uint32_t m = top8(v);
+#pragma unroll
+    for (int off = 1; off < 16; off <<= 1) m = max(m, (uint32_t)__shfl_xor((int)m, off));
+    const Scale sc = scale_of(m);
+    if (c < K) *reinterpret_cast<uint2*>(q + row * K + c) = quantize8(v, sc);
+    if (threadIdx.x % 16 == 0) scales[b] = sc.s;
+  }
+}
+
+// A scale per 128 x 128 values: a workgroup to a block, a thread holds 8 values of 8 rows.
+template <typename XT>
+__global__ __launch_bounds__(kThreads) void quantize_blocks_kernel(const XT* x, int64_t rows, int K, int kb, uint8_t* q,
+                                                                   float* scales) {
+  __shared__ uint32_t part[2][kThreads / kWave];
+  const int64_t blocks = (rows + 127) / 128 * kb;
+  int parity = 0;  // two buffers in turn: a wave may write the next block's part while another still reads this one's
+  for (int64_t b = blockIdx.x; b < blocks; b += gridDim.x, parity ^= 1) {
+    const int64_t rb = b / kb, r0 = 128 * rb + threadIdx.x / 16;
+    const int c = 128 * (int)(b - rb * kb) + 8 * (threadIdx.x % 16);
+    float v[8][8];
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) v[i][k] = 0.f;
+      if (c < K && r0 + 16 * i < rows) load8(x + (r0 + 16 * i) * K + c, v[i]);
+      m = max(m, top8(v[i]));
+    }
+#pragma unroll
+    for (int off = 1; off < kWave; off <<= 1) m = max(m, (uint32_t)__shfl_xor((int)m, off));
+    if (wave_lane() == 0) part[parity][threadIdx.x / kWave] = m;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kThreads / kWave; ++i) m = max(m, part[parity][i]);
+    const Scale sc = scale_of(m);
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (c < K && r0 + 16 * i < rows) *reinterpret_cast<uint2*>(q + (r0 + 16 * i) * K + c) = quantize8(v[i], sc);
+    if (threadIdx.x == 0) scales[b] = sc.s;
+  }
+}
+
+template <typename XT>
+hipError_t go(const XT* x, int64_t rows, int K, int by, uint8_t* q, float* scales, hipStream_t s) {
+  const int kb = (K + 127) / 128;
+  const int64_t want = by == 1 ? (rows * kb + kThreads / 16 - 1) / (kThreads / 16) : (rows + 127) / 128 * kb;
+  const unsigned grid = (unsigned)(want < (1 << 20) ? want : 1 << 20);
+  if (by == 1)
+    quantize_rows_kernel<XT><<<grid, kThreads, 0, s>>>(x, rows, K, kb, q, scales);
+  else
+    quantize_blocks_kernel<XT><<<grid, kThreads, 0, s>>>(x, rows, K, kb, q, scales);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_fp8_quantize(const void* x, bool x_f32, int64_t rows, int K, int by, uint8_t* q, float* scales,
+                               hipStream_t s) {
+  return x_f32 ? go(static_cast<const float*>(x), rows, K, by, q, scales, s)
+               : go(static_cast<const uint16_t*>(x), rows, K, by, q, scales, s);
+}
+
+}  // namespace bitmoe

@@ -1,0 +1,156 @@
+// Gradients of a bf16 product y = x W^T and of the gated projection h = act(g) u, [g | u] = x W^T:
+//   dx = dy W (a sum over the weight rows), dW = dy^T x (a sum over the tokens)
+//   dg = dh u act'(g), du = dh act(g), and dy = [dg | du]
+// The sums run along the rows of one operand or of both; the operands are transposed into the workspace and
+// go through the dense product.
+#include <algorithm>
+
+#include "../common.h"
+#include "block_kernels.h"
+#include "linear_dev.h"
+
+namespace bitmoe {
+
+namespace {
+
+constexpr int kThreads = 256;
+
+// src [R][C] -> dst [C][pitch], the columns from R to pitch (R rounded up to 8) zero.  A workgroup moves 64 x 64.
+__global__ __launch_bounds__(kThreads) void transpose_kernel(const uint16_t* src, int R, int C, int pitch, int c_tiles,
+                                                             uint16_t* dst) {
+  __shared__ uint16_t tile[64][66];
+  const int r0 = 64 * (int)(blockIdx.x / c_tiles), c0 = 64 * (int)(blockIdx.x % c_tiles);
+  const int j = threadIdx.x % 64;
+  for (int i = threadIdx.x / 64; i < 64; i += kThreads / 64)
+    tile[i][j] = r0 + i < R && c0 + j < C ? src[(int64_t)(r0 + i) * C + c0 + j] : (uint16_t)0;
+  __syncthreads();
+  for (int i = threadIdx.x / 64; i < 64; i += kThreads / 64)
+    if (c0 + i < C && r0 + j < pitch) dst[(int64_t)(c0 + i) * pitch + r0 + j] = tile[j][i];
+}
+
+hipError_t transpose(const uint16_t* src, int64_t R, int64_t C, uint16_t* dst, hipStream_t s) {
+  const int64_t pitch = (R + 7) / 8 * 8, r_tiles = (pitch + 63) / 64, c_tiles = (C + 63) / 64;
+  transpose_kernel<<<(unsigned)(r_tiles * c_tiles), kThreads, 0, s>>>(src, (int)R, (int)C, (int)pitch, (int)c_tiles, dst);
+  return hipGetLastError();
+}
+
+size_t up256(size_t n) { return (n + 255) / 256 * 256; }
+size_t transposed(int64_t R, int64_t C) { return up256((size_t)C * ((R + 7) / 8 * 8) * 2); }
+
+__global__ __launch_bounds__(kThreads) void fill_kernel(uint32_t* p, int64_t n) {
+  for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < n; i += (int64_t)gridDim.x * kThreads) p[i] = 0;
+}
+
+// act(g) and act'(g) in fp32
+template <int ACT>
+__device__ __forceinline__ void act_slope(float g, float& value, float& slope) {
+  if constexpr (ACT == kActNone) {
+    value = g, slope = 1.0f;
+  } else if constexpr (ACT == kActRelu) {
+    value = g < 0.0f ? 0.0f : g, slope = g > 0.0f ? 1.0f : 0.0f;
+  } else if constexpr (ACT == kActSilu) {
+    const float p = __builtin_amdgcn_rcpf(1.0f + __expf(-g));
+    value = g * p, slope = fmaf(value, 1.0f - p, p);
+  } else {
+    // g p with p = 1 / (1 + exp(-z)), z = 2 sqrt(2/pi) (g + 0.044715 g^3)
+    const float z = 1.5957691216057308f * g * fmaf(0.044715f * g, g, 1.0f);
+    const float p = __builtin_amdgcn_rcpf(1.0f + __expf(-z)), t = p * (1.0f - p);
+    const float dz = 1.5957691216057308f * fmaf(0.134145f * g, g, 1.0f);
+    value = g * p, slope = t > 0.0f ? fmaf(g * t, dz, p) : p;  // t = 0 where dz may be infinite
+  }
+}
+
+// eight bf16 values
+__device__ __forceinline__ void load8(const uint16_t* p, float (&v)[8]) {
+  const uint4 a = *reinterpret_cast<const uint4*>(p);
+  const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    v[2 * i] = bf16_to_f32(w[i] & 0xFFFFu);
+    v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+  }
+}
+__device__ __forceinline__ void store8(uint16_t* p, const float (&v)[8]) {
+  *reinterpret_cast<uint4*>(p) = make_uint4(f32x2_to_bf16x2_rne(v[0], v[1]), f32x2_to_bf16x2_rne(v[2], v[3]),
+                                            f32x2_to_bf16x2_rne(v[4], v[5]), f32x2_to_bf16x2_rne(v[6], v[7]));
+}
+
+// The matrix cores take the gradients of the pre-activations as bf16: one rounding, of the size of the outputs' own.
+template <int ACT>
+__global__ __launch_bounds__(kThreads) void glu_grad_kernel(const uint16_t* dh, const uint16_t* a, int T, int I,
+                                                            uint16_t* da) {
+  const int per = I / 8;
+  const int64_t n = (int64_t)T * per;
+  for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < n; i += (int64_t)gridDim.x * kThreads) {
+    const int64_t t = i / per, at = t * 2 * I + 8 * (i - t * per);
+    float d[8], g[8], u[8], dg[8], du[8];
+    load8(dh + 8 * i, d);
+    load8(a + at, g);
+    load8(a + at + I, u);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      float value, slope;
+      act_slope<ACT>(g[j], value, slope);
+      dg[j] = d[j] * u[j] * slope;
+      du[j] = d[j] * value;
+    }
+    store8(da + at, dg);
+    store8(da + at + I, du);
+  }
+}
+
+hipError_t product(const uint16_t* x, const uint16_t* w, int64_t T, int64_t N, int64_t K, void* out, int out_f32,
+                   bool add, hipStream_t s) {
+  LinearArgs a{};
+  a.x = reinterpret_cast<const uint8_t*>(x);
+  a.w = reinterpret_cast<const uint8_t*>(w);
+  a.out = out;
+  a.residual = add ? out : nullptr;
+  a.T = (int)T, a.N = a.n_out = (int)N, a.K = (int)K;
+  a.act = kActNone;
+  a.res_f32 = a.out_f32 = out_f32;
+  a.vec = N % 4 == 0 && reinterpret_cast<uintptr_t>(out) % (out_f32 ? 16 : 8) == 0;
+  return launch_linear(a, kBf16, s);
+}
+
+}  // namespace
+
+size_t grad_ws_bytes(int64_t T, int64_t N, int64_t K) {
+  return transposed(N, K) + transposed(T, N) + transposed(T, K);
+}
+
+hipError_t launch_grad(const GradArgs& a, uint8_t* ws, hipStream_t s) {
+  const int64_t T = a.T, N = a.N, K = a.K, Tp = (T + 7) / 8 * 8;
+  uint16_t* wt = reinterpret_cast<uint16_t*>(ws);
+  uint16_t* dyt = reinterpret_cast<uint16_t*>(ws + transposed(N, K));
+  uint16_t* xt = reinterpret_cast<uint16_t*>(ws + transposed(N, K) + transposed(T, N));
+  hipError_t e = hipSuccess;
+  if (a.dx && T > 0) {
+    if ((e = transpose(a.w, N, K, wt, s)) != hipSuccess) return e;
+    if ((e = product(a.dy, wt, T, K, N, a.dx, a.dx_f32, false, s)) != hipSuccess) return e;
+  }
+  if (a.dw && T > 0) {
+    if ((e = transpose(a.dy, T, N, dyt, s)) != hipSuccess) return e;
+    if ((e = transpose(a.x, T, K, xt, s)) != hipSuccess) return e;
+    return product(dyt, xt, N, K, Tp, a.dw, a.dw_f32, a.accumulate, s);
+  }
+  if (a.dw && !a.accumulate) {
+    const int64_t words = N * K / (a.dw_f32 ? 1 : 2);
+    fill_kernel<<<(unsigned)std::min<int64_t>(1024, (words + kThreads - 1) / kThreads), kThreads, 0, s>>>(
+        static_cast<uint32_t*>(a.dw), words);
+    return hipGetLastError();
+  }
+  return e;
+}
+
+hipError_t launch_glu_grad(const uint16_t* dh, const uint16_t* a, int T, int I, int act, uint16_t* da, hipStream_t s) {
+  const int64_t want = ((int64_t)T * (I / 8) + kThreads - 1) / kThreads;
+  const unsigned grid = (unsigned)std::min<int64_t>(want, 1 << 20);
+  if (act == kActNone) glu_grad_kernel<kActNone><<<grid, kThreads, 0, s>>>(dh, a, T, I, da);
+  if (act == kActRelu) glu_grad_kernel<kActRelu><<<grid, kThreads, 0, s>>>(dh, a, T, I, da);
+  if (act == kActGelu) glu_grad_kernel<kActGelu><<<grid, kThreads, 0, s>>>(dh, a, T, I, da);
+  if (act == kActSilu) glu_grad_kernel<kActSilu><<<grid, kThreads, 0, s>>>(dh, a, T, I, da);
+  return hipGetLastError();
+}
+
+}  // namespace bitmoe

@@ -25,7 +25,7 @@ namespace {
 constexpr int kXcds = 8;
 constexpr int kRow = 128;                          // bytes of a row in a stage
 constexpr int kRows = 1024 / kRow, kChunks = kRow / 16;  // rows of a load, 16-byte chunks of a row
-template <bool MX, bool GATED, int BM, int BN, int WM, int WN, int WK, int S, int OCC, int kSpread>
+template <bool MX, int GATED, int BM, int BN, int WM, int WN, int WK, int S, int OCC, int kSpread>
 __global__ __launch_bounds__(64 * WM * WN * WK, OCC) void linear_tile_kernel(LinearArgs a, int m_tiles, int n_tiles) {
   constexpr int NW = WM * WN, kThreads = 64 * NW;      // of one K group
   constexpr int AT = BM / WM / 32, BT = BN / WN / 32;   // token and weight MFMA tiles of a wave
@@ -419,7 +419,7 @@ __global__ __launch_bounds__(64 * WM * WN * WK, OCC) void linear_tile_kernel(Lin
   }
 }
 
-template <bool MX, bool GATED, int BM, int BN, int WM, int WN, int WK, int S, int OCC, int kSpread>
+template <bool MX, int GATED, int BM, int BN, int WM, int WN, int WK, int S, int OCC, int kSpread>
 hipError_t go_tile(const LinearArgs& a, hipStream_t s) {
   const int64_t m_tiles = ((int64_t)a.T + BM - 1) / BM;
   const int bn = GATED ? BN / 2 : BN, n_tiles = (a.n_out + bn - 1) / bn;
@@ -476,10 +476,10 @@ Variant choose(const LinearArgs& a) {
   return best;
 }
 
-template <bool MX, bool GATED>
+template <bool MX, int GATED>
 hipError_t launch(const LinearArgs& a, hipStream_t s) {
   const Variant v = choose<MX>(a);
-  if (v <= kRows64) return launch_linear_rows(a, MX, v == kRows16 ? 1 : v == kRows32 ? 2 : 4, s);
+  if (v <= kRows64) return launch_linear_rows(a, MX ? kMxfp8 : kBf16, v == kRows16 ? 1 : v == kRows32 ? 2 : 4, s);
   if (v == kTile64) return go_tile<MX, GATED, 64, 64, 2, 2, 1, 4, 2, 1>(a, s);
   if (v == kTile128) return go_tile<MX, GATED, 128, 128, 2, 2, 1, 2, 2, 1>(a, s);
   if constexpr (MX) return go_tile<MX, GATED, 64, 64, 2, 2, 2, 4, 2, 1>(a, s);
@@ -492,10 +492,12 @@ hipError_t launch(const LinearArgs& a, hipStream_t s) {
 
 }  // namespace
 
-hipError_t launch_linear(const LinearArgs& a, bool mxfp8, hipStream_t s) {
+hipError_t launch_linear(const LinearArgs& a, LinearKind kind, hipStream_t s) {
   const bool gated = a.act == kActSwiglu;
-  if (mxfp8) return gated ? launch<true, true>(a, s) : launch<true, false>(a, s);
-  return gated ? launch<false, true>(a, s) : launch<false, false>(a, s);
+  if (kind == kFp8) return launch_linear_rows(a, kFp8, a.T <= 16 ? 1 : a.T <= 32 ? 2 : 4, s);
+  if (kind == kMxfp8) return gated ? launch<true, kSwiglu>(a, s) : launch<true, kPlain>(a, s);
+  if (a.act == kActGlu) return launch<false, kGlu>(a, s);
+  return gated ? launch<false, kSwiglu>(a, s) : launch<false, kPlain>(a, s);
 }
 
 }  // namespace bitmoe

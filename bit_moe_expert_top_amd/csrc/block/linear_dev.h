@@ -27,6 +27,14 @@ __device__ __forceinline__ f32x16_t mfma_mxfp8_32x32x64(u32x4 a0, u32x4 a1, u32x
   const i32x8 b = {(int)b0[0], (int)b0[1], (int)b0[2], (int)b0[3], (int)b1[0], (int)b1[1], (int)b1[2], (int)b1[3]};
   return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a, b, c, 0, 0, 0, (int)sa, 0, (int)sb);
 }
+// D(16x16, f32) += A(16x128, e4m3) * B(128x16, e4m3) without scales (scale operands of 0 select that instruction): lane l
+// supplies row l % 16, k = 64 c + 16 (l / 16) + [0, 16) in its 16-byte chunks c = 0, 1 and receives D[4 (l / 16) + i][l % 16].
+// Its sums are as near as those of the instruction above.
+__device__ __forceinline__ f32x4 mfma_fp8_16x16x128(u32x4 a0, u32x4 a1, u32x4 b0, u32x4 b1, f32x4 c) {
+  const i32x8 a = {(int)a0[0], (int)a0[1], (int)a0[2], (int)a0[3], (int)a1[0], (int)a1[1], (int)a1[2], (int)a1[3]};
+  const i32x8 b = {(int)b0[0], (int)b0[1], (int)b0[2], (int)b0[3], (int)b1[0], (int)b1[1], (int)b1[2], (int)b1[3]};
+  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, c, 0, 0, 0, 0, 0, 0);
+}
 
 typedef __attribute__((address_space(3))) void lds_void;
 
@@ -97,11 +105,11 @@ __device__ __forceinline__ Four load_residual4(const LinearArgs& a, int64_t at, 
   return r;
 }
 
-// The bias of four columns (and of their up rows with SwiGLU), zero without one.
+// The bias of four columns (and of their up rows with a gate), zero without one.
 struct FourBias {
   float g[4], u[4];
 };
-template <bool GATED>
+template <int GATED>
 __device__ __forceinline__ FourBias load_bias4(const LinearArgs& a, int n) {
   FourBias b;
 #pragma unroll
@@ -113,18 +121,42 @@ __device__ __forceinline__ FourBias load_bias4(const LinearArgs& a, int n) {
   return b;
 }
 
-// v (and, with SwiGLU, the up columns u): the sums without bias.  Adds the bias, applies the
+// What becomes of the weight rows' halves: kPlain no halves, kSwiglu silu(gate) * up, kGlu act(gate) * up with the
+// activation a.glu_act and, where a.pre is given, the pre-activations stored (rounded to bf16) for the backward pass.
+constexpr int kPlain = 0, kSwiglu = 1, kGlu = 2;
+
+// Four bf16 values to p, of which cols lie inside the row.
+__device__ __forceinline__ void store_bf16x4(uint16_t* p, const float (&v)[4], bool vec, int cols) {
+  if (vec) {
+    *reinterpret_cast<u32x2*>(p) = u32x2{f32x2_to_bf16x2_rne(v[0], v[1]), f32x2_to_bf16x2_rne(v[2], v[3])};
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    if (i < cols) p[i] = (uint16_t)f32_to_bf16_rne(v[i]);
+}
+
+// v (and, with a gate, the up columns u): the sums without bias.  Adds the bias, applies the
 // activation, adds the residual and stores, rounding once.  STREAM: non-temporal stores, for the larger tiles, whose
 // outputs are larger than the caches (with buffers that change from call to call, 8192 x 4096 in bf16, K = 4096:
 // 227 -> 220 us, SwiGLU 219 -> 216; in MXFP8, K = 2048: 106 -> 88, with a bf16 residual 112 -> 108; with the same
 // buffers each time 2 % at most).
-template <bool GATED, bool STREAM>
+template <int GATED, bool STREAM>
 __device__ __forceinline__ void epilogue4(const LinearArgs& a, int64_t at, int n, const float (&v)[4],
                                           const float (&u)[4], const FourBias& bias, const Four& res) {
   float r[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) r[i] = v[i] + bias.g[i];
-  if constexpr (GATED) {
+  if constexpr (GATED == kGlu) {
+    if (a.pre) {
+      uint16_t* gate = a.pre + 2 * at - n;  // row t of 2 n_out columns, at = t n_out + n
+      store_bf16x4(gate, v, a.vec, a.n_out - n);
+      store_bf16x4(gate + a.n_out, u, a.vec, a.n_out - n);
+    }
+    activate(r, a.glu_act);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) r[i] *= u[i];
+  } else if constexpr (GATED == kSwiglu) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) r[i] = silu_f32(r[i]) * (u[i] + bias.u[i]);
   } else {

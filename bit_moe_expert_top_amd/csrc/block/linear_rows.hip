@@ -29,9 +29,10 @@ __device__ __forceinline__ f32x4 mfma_mxfp8_16x16x128(u32x4 a0, u32x4 a1, u32x4 
 
 // NW waves, U runs of K in flight per wave, XR token rows in a slot (16 TT, or 8 for at most 8 tokens:
 // the matrix cores' other token columns then repeat them, and are not stored)
-template <bool MX, bool GATED, int TT, int NW, int U, int XR>
+template <LinearKind KIND, int GATED, int TT, int NW, int U, int XR>
 __global__ __launch_bounds__(64 * NW, NW / 4) void linear_rows_kernel(LinearArgs a, int n_tiles) {
-  constexpr int kEs = MX ? 1 : 2, kRun = 128, kRows = 16 + XR, kSlot = kRows * kRun;
+  constexpr bool MX = KIND == kMxfp8, FP8 = KIND == kFp8;
+  constexpr int kEs = KIND == kBf16 ? 2 : 1, kRun = 128, kRows = 16 + XR, kSlot = kRows * kRun;
   constexpr int LD = kRows / 8;               // direct loads per run
   constexpr int kSc = (kRows + 63) / 64;      // scale dwords per lane and run
   static_assert(U >= 2 && U <= 4 && NW >= TT && TT * 1024 <= kSlot, "shape");
@@ -42,7 +43,7 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void linear_rows_kernel(LinearArgs
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   const int64_t t0 = (int64_t)(blockIdx.x / n_tiles) * (16 * TT);
   const int n0 = (int)(blockIdx.x % n_tiles) * (GATED ? 8 : 16);
-  const int kb_bytes = a.K * kEs, ks = a.K / 32, runs = (kb_bytes + kRun - 1) / kRun;
+  const int kb_bytes = a.K * kEs, ks = FP8 ? (a.K + 127) / 128 * 4 : a.K / 32, runs = (kb_bytes + kRun - 1) / kRun;
   // resources that end with the tile's last row: weight rows 0-7 and 8-15 (gate and up with SwiGLU)
   // and the tokens; what lies past them, or past K, has an offset past the resource and reads zeros
   const int rows_x = (int)min((int64_t)(16 * TT), a.T - t0);
@@ -59,17 +60,20 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void linear_rows_kernel(LinearArgs
     const bool in = i == 0 ? row8 < rows_w0 : i == 1 ? row8 < rows_w1 : 8 * (i - 2) + row8 < rows_x;
     off[i] = in ? (uint32_t)(i < 2 ? row8 : 8 * (i - 2) + row8) * kb_bytes + (uint32_t)ch[i & 1] : kOffNone;
   }
-  // MXFP8: lane l fetches the four scales of a run of slot rows l and 64 + l
+  // MXFP8: lane l fetches the four scales of a run of slot rows l and 64 + l; FP8: their one fp32 scale (ks: bytes of a
+  // row of scales, four for a run in both).  The 8 weight rows of a half lie in one block row.
+  const int up_blocks = (a.n_out + 127) / 128;  // block rows of the gate
   const uint8_t* srow[kSc];
-  if (MX) {
+  if (MX || FP8) {
 #pragma unroll
     for (int c = 0; c < kSc; ++c) {
       const int r = lane + 64 * c;
       srow[c] = nullptr;
       if (r < 8) {
-        if (r < rows_w0) srow[c] = a.w_scales + ((int64_t)n0 + r) * ks;
+        if (r < rows_w0) srow[c] = a.w_scales + (FP8 ? (int64_t)(n0 / 128) : (int64_t)n0 + r) * ks;
       } else if (r < 16) {
-        if (r - 8 < rows_w1) srow[c] = a.w_scales + (w1 + r - 8) * ks;
+        if (r - 8 < rows_w1)
+          srow[c] = a.w_scales + (FP8 ? (int64_t)((GATED ? up_blocks : 0) + n0 / 128) : w1 + r - 8) * ks;
       } else if (r - 16 < rows_x) {
         srow[c] = a.x_scales + (t0 + r - 16) * ks;
       }
@@ -79,13 +83,13 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void linear_rows_kernel(LinearArgs
   auto slot = [&](int u) -> uint8_t* { return (u == 0 ? s0 : u == 1 ? s1 : u == 2 ? s2 : s3) + w * kSlot; };
   auto load = [&](int u, int run) {
     const int b = run * kRun;
-    if (MX) {
+    if (MX || FP8) {
 #pragma unroll
       for (int c = 0; c < kSc; ++c) {
         uint32_t v = 0;
         if (srow[c]) {
           const int left = ks - 4 * run;
-          if (left >= 4) {
+          if (FP8 || left >= 4) {
             __builtin_memcpy(&v, srow[c] + 4 * run, 4);
           } else {
             for (int i = 0; i < left; ++i) v |= (uint32_t)srow[c][4 * run + i] << (8 * i);
@@ -132,6 +136,17 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void linear_rows_kernel(LinearArgs
       for (int t = 0; t < TT; ++t) {
         const uint32_t sx = scale(t + 1);
         acc[t] = mfma_mxfp8_16x16x128(wv[0], wv[1], xv[t][0], xv[t][1], acc[t], sw, sx);
+      }
+    } else if constexpr (FP8) {
+      // a run is one block of K: its sum by itself, then times both scales into the fp32 sum
+      const float sw = __int_as_float(__builtin_amdgcn_ds_bpermute(4 * (4 * g), (int)sreg[u][0]));
+#pragma unroll
+      for (int t = 0; t < TT; ++t) {
+        const int i = t + 1;
+        const float sc = sw * __int_as_float(__builtin_amdgcn_ds_bpermute(4 * (16 * (i % 4) + r16), (int)sreg[u][i / 4]));
+        const f32x4 p = mfma_fp8_16x16x128(wv[0], wv[1], xv[t][0], xv[t][1], f32x4{0.f, 0.f, 0.f, 0.f});
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc[t][j] = fmaf(sc, p[j], acc[t][j]);
       }
     } else {
 #pragma unroll
@@ -187,29 +202,31 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void linear_rows_kernel(LinearArgs
   epilogue4<GATED, false>(a, at, n, v, u, load_bias4<GATED>(a, n), res);
 }
 
-template <bool MX, bool GATED, int TT, int NW, int U, int XR = 16 * TT>
+template <LinearKind KIND, int GATED, int TT, int NW, int U, int XR = 16 * TT>
 hipError_t go_rows(const LinearArgs& a, hipStream_t s) {
   const int per = GATED ? 8 : 16, n_tiles = (a.n_out + per - 1) / per;
   const int64_t m_tiles = ((int64_t)a.T + 16 * TT - 1) / (16 * TT);
-  linear_rows_kernel<MX, GATED, TT, NW, U, XR><<<(unsigned)(m_tiles * n_tiles), 64 * NW, 0, s>>>(a, n_tiles);
+  linear_rows_kernel<KIND, GATED, TT, NW, U, XR><<<(unsigned)(m_tiles * n_tiles), 64 * NW, 0, s>>>(a, n_tiles);
   return hipGetLastError();
 }
 
-template <bool MX, bool GATED>
+template <LinearKind KIND, int GATED>
 hipError_t launch(const LinearArgs& a, int tt, hipStream_t s) {
   // 1 x 4096 x 4096: 7.8 us with 8 token rows in a slot, 8.2 us with 16; 1 x 384 x 4096: 4.1 and 4.6 us
-  if (tt == 1 && a.T <= 8) return go_rows<MX, GATED, 1, 8, 3, 8>(a, s);
-  if (tt == 1) return go_rows<MX, GATED, 1, 8, 4>(a, s);
-  if (tt == 2) return go_rows<MX, GATED, 2, 8, 3>(a, s);
-  return go_rows<MX, GATED, 4, 4, 3>(a, s);
+  if (tt == 1 && a.T <= 8) return go_rows<KIND, GATED, 1, 8, 3, 8>(a, s);
+  if (tt == 1) return go_rows<KIND, GATED, 1, 8, 4>(a, s);
+  if (tt == 2) return go_rows<KIND, GATED, 2, 8, 3>(a, s);
+  return go_rows<KIND, GATED, 4, 4, 3>(a, s);
 }
 
 }  // namespace
 
-hipError_t launch_linear_rows(const LinearArgs& a, bool mxfp8, int tt, hipStream_t s) {
+hipError_t launch_linear_rows(const LinearArgs& a, LinearKind kind, int tt, hipStream_t s) {
   const bool gated = a.act == kActSwiglu;
-  if (mxfp8) return gated ? launch<true, true>(a, tt, s) : launch<true, false>(a, tt, s);
-  return gated ? launch<false, true>(a, tt, s) : launch<false, false>(a, tt, s);
+  if (kind == kMxfp8) return gated ? launch<kMxfp8, kSwiglu>(a, tt, s) : launch<kMxfp8, kPlain>(a, tt, s);
+  if (kind == kFp8) return gated ? launch<kFp8, kSwiglu>(a, tt, s) : launch<kFp8, kPlain>(a, tt, s);
+  if (a.act == kActGlu) return launch<kBf16, kGlu>(a, tt, s);
+  return gated ? launch<kBf16, kSwiglu>(a, tt, s) : launch<kBf16, kPlain>(a, tt, s);
 }
 
 }  // namespace bitmoe

@@ -442,6 +442,74 @@ moe_status moe_route_scored(const float* logits, const float* bias, int32_t T, i
                             int32_t score, int32_t n_group, int32_t topk_group, int32_t group_top,
                             int32_t renormalize, float scale, int32_t* topk_ids, float* topk_w, void* stream);
 
+/* moe_fp8_quantize -- FP8 (e4m3fn) with an fp32 scale for each block of 128: of block_rows x 128 values, block_rows = 1
+ * (activations: a scale per row and 128 of K) or 128 (weights).
+ *     scale = max|x| / 448,  q = x / scale rounded to e4m3 (nearest even), both divisions in fp32
+ *   x        [rows][K], MOE_DT_F32 or MOE_DT_BF16 (x_dtype)
+ *   q        u8 [rows][K]
+ *   scales   f32 [rows / block_rows rounded up][K / 128 rounded up]; the last blocks may be partial
+ * A block of zeros, or of values so small that their scale is 0, has scale 0 and elements 0.  An infinity makes its
+ * block's scale infinite (its own element NaN, the others 0), a NaN makes scale and elements NaN.
+ * Errors: INVALID_ARG (bad sizes, types or pointers; x not 16-byte, q not 8-byte, scales not 4-byte aligned),
+ * UNSUPPORTED (K % 16 != 0; K > 2^20; rows > 2^26). */
+moe_status moe_fp8_quantize(const void* x, int32_t x_dtype, int64_t rows, int32_t K, int32_t block_rows, uint8_t* q,
+                            float* scales, void* stream);
+
+/* moe_linear_fp8 -- moe_linear of FP8 operands with a scale for each block of 128:
+ *     a[t][n] = sum over blocks b of K: x_scales[t][b] * w_scales[n's block row][b] * (sum over k in b of x[t][k] w[n][k])
+ *     out     = act(a + bias) + residual, rounded once to bf16
+ *   x, x_scales    u8 [T][K] e4m3fn, f32 [T][K/128 rounded up]      (moe_fp8_quantize, block_rows 1)
+ *   w, w_scales    u8 [N][K] e4m3fn, f32 [block rows][K/128 rounded up]   (moe_fp8_quantize, block_rows 128); block rows
+ *                  are runs of 128 rows of w.  MOE_ACT_SWIGLU: gate and up are two matrices of N/2 rows, one behind
+ *                  the other, and so are their scales: 2 * (N/2/128 rounded up) block rows
+ *   bias, act, residual, residual_dtype   as moe_linear
+ *   out            bf16 [T][N, or N/2 with SwiGLU]; may be a bf16 residual itself
+ * A block's products are summed by the FP8 matrix cores (not an fp32 sum: see moe_linear), the blocks in fp32.  The order
+ * of a row's sums may follow T, so its bits may change with the batch size.
+ * Errors: INVALID_ARG (bad sizes, types or pointers; N odd with SwiGLU; x or w not 16-byte aligned; out over part of
+ * residual), UNSUPPORTED (K % 16 != 0; N or K > 2^20; T > 2^26). */
+moe_status moe_linear_fp8(const uint8_t* x, const float* x_scales, const uint8_t* w, const float* w_scales, int32_t T,
+                          int32_t N, int32_t K, const float* bias, int32_t act, const void* residual,
+                          int32_t residual_dtype, uint16_t* out, void* stream);
+
+/* moe_glu -- the gated projection of a feed-forward block, both products, the activation and the gating in one launch:
+ *     [g | u] = x W^T,  h = act(g) * u
+ *   x bf16 [T][K], w bf16 [2I][K] (gate rows first, the layout of an expert's W1), h bf16 [T][I]
+ *   act   MOE_ACT_NONE, RELU, GELU or SILU
+ *   a     bf16 [T][2I], the pre-activations [g | u] for moe_glu_backward, or NULL
+ * h is computed from the unrounded fp32 sums.  Nothing may overlap.  The order of a row's sums may follow T.
+ * Errors: INVALID_ARG (bad sizes or pointers; a pointer not 16-byte aligned; an output over another array),
+ * UNSUPPORTED (K % 8 != 0; I % 8 != 0; 2 I or K > 2^20; T > 2^26). */
+moe_status moe_glu(const uint16_t* x, const uint16_t* w, int32_t T, int32_t I, int32_t K, int32_t act, uint16_t* a,
+                   uint16_t* h, void* stream);
+
+/* moe_linear_backward -- the gradients of y = x W^T:
+ *     dx = dy W,   dw = dy^T x  (added to what dw holds if accumulate)
+ *   dy bf16 [T][N], x bf16 [T][K], w bf16 [N][K]
+ *   dx    [T][K] of dx_dtype (F32 or BF16), or NULL (then w may be NULL)
+ *   dw    [N][K] of dw_dtype (F32 or BF16), or NULL (then x may be NULL); not both NULL
+ *   ws    moe_linear_backward_ws_bytes(T, N, K) bytes, 16-byte aligned
+ * Sums are fp32 on the matrix cores, rounded once; the same call gives the same bits.  T = 0 leaves dw zero (or, with
+ * accumulate, as it is).  No output may overlap an input, the other output or the workspace.
+ * moe_linear_backward_ws_bytes returns 0 for sizes that the call refuses.
+ * Errors: INVALID_ARG (bad sizes, types or pointers; a pointer not 16-byte aligned; overlaps), WORKSPACE (ws_bytes too
+ * small), UNSUPPORTED (N or K % 8 != 0, N or K > 2^20, T > 2^20). */
+size_t moe_linear_backward_ws_bytes(int32_t T, int32_t N, int32_t K);
+moe_status moe_linear_backward(const uint16_t* dy, const uint16_t* x, const uint16_t* w, int32_t T, int32_t N, int32_t K,
+                               void* dx, int32_t dx_dtype, void* dw, int32_t dw_dtype, int32_t accumulate, void* ws,
+                               size_t ws_bytes, void* stream);
+
+/* moe_glu_backward -- the gradients of moe_glu:
+ *     dg = dh * u * act'(g),  du = dh * act(g)   (fp32 from the bf16 a and dh, then rounded to bf16 for the matrix cores)
+ *     dx = [dg | du] W,  dw = [dg | du]^T x (+ dw if accumulate)
+ *   dh bf16 [T][I], a bf16 [T][2I] as moe_glu wrote it, x bf16 [T][K], w bf16 [2I][K]; dx, dw and the rest as
+ *   moe_linear_backward with N = 2I; ws: moe_glu_backward_ws_bytes(T, I, K) bytes.  relu'(0) = 0.
+ * Errors: as moe_linear_backward and moe_glu. */
+size_t moe_glu_backward_ws_bytes(int32_t T, int32_t I, int32_t K);
+moe_status moe_glu_backward(const uint16_t* dh, const uint16_t* a, const uint16_t* x, const uint16_t* w, int32_t T,
+                            int32_t I, int32_t K, int32_t act, void* dx, int32_t dx_dtype, void* dw, int32_t dw_dtype,
+                            int32_t accumulate, void* ws, size_t ws_bytes, void* stream);
+
 /* moe_debug_dequant -- decode one low-bit expert matrix with the same device code the FFN
  * kernels use, into f32[rows][K] (W1: rows = 2I, K = H; W2: rows = H, K = I), in natural K
  * order.  For tests: the decoded weights must equal the format definition bit for bit.

@@ -1,0 +1,152 @@
+"""Refusals of the FP8 block-scaled product and its quantiser, the gated projection and the gradient calls: every
+check fails on the host before anything is enqueued, so no GPU is needed; and the binding's own checks."""
+import pytest
+import torch
+
+
+@pytest.fixture(scope="module")
+def L():
+    from bit_moe_expert_top_amd import _lib
+
+    return _lib
+
+
+def at(i):
+    """A 4096-byte aligned address that is never dereferenced, 16 MiB from the others."""
+    return (i + 1) << 24
+
+
+X, XS, W, WS, B, R, O, A, D, DX, DW, S = (at(i) for i in range(12))
+
+
+def quantize(L, x=X, dt=2, rows=4, K=64, by=1, q=O, s=XS):
+    return L.lib.moe_fp8_quantize(x, dt, rows, K, by, q, s, None)
+
+
+@pytest.mark.parametrize("bad,want", [
+    (dict(rows=-1), -1), (dict(K=0), -1), (dict(dt=3), -1), (dict(dt=0), -1), (dict(by=0), -1), (dict(by=64), -1),
+    (dict(K=72), -2), (dict(K=(1 << 20) + 16), -2), (dict(rows=(1 << 26) + 1), -2), (dict(x=None), -1), (dict(q=None), -1),
+    (dict(s=None), -1), (dict(x=X + 8), -1), (dict(q=O + 4), -1), (dict(s=XS + 2), -1),
+])
+def test_quantize_refusals(L, bad, want):
+    assert quantize(L, **bad) == want
+
+
+def fp8(L, x=X, xs=XS, w=W, ws=WS, T=4, N=64, K=64, bias=B, act=0, r=R, rd=1, out=O):
+    return L.lib.moe_linear_fp8(x, xs, w, ws, T, N, K, bias, act, r, rd, out, None)
+
+
+@pytest.mark.parametrize("bad,want", [
+    (dict(T=-1), -1), (dict(N=0), -1), (dict(K=0), -1), (dict(act=-1), -1), (dict(act=5), -1), (dict(rd=3), -1),
+    (dict(act=4, N=63), -1), (dict(K=72), -2), (dict(K=(1 << 20) + 16), -2), (dict(N=(1 << 20) + 1), -2),
+    (dict(T=(1 << 26) + 1), -2), (dict(x=None), -1), (dict(xs=None), -1), (dict(w=None), -1), (dict(ws=None), -1),
+    (dict(out=None), -1), (dict(x=X + 8), -1), (dict(w=W + 4), -1), (dict(xs=XS + 2), -1), (dict(ws=WS + 1), -1),
+    (dict(bias=B + 2), -1), (dict(out=O + 1), -1), (dict(r=R + 2), -1), (dict(r=O), -1), (dict(r=O + 2, rd=2), -1),
+])
+def test_fp8_product_refusals(L, bad, want):
+    assert fp8(L, **bad) == want
+
+
+def glu(L, x=X, w=W, T=4, I=64, K=64, act=3, a=A, h=O):
+    return L.lib.moe_glu(x, w, T, I, K, act, a, h, None)
+
+
+@pytest.mark.parametrize("bad,want", [
+    (dict(T=-1), -1), (dict(I=0), -1), (dict(K=-8), -1), (dict(act=4), -1), (dict(act=-1), -1), (dict(K=60), -2),
+    (dict(I=60), -2), (dict(K=(1 << 20) + 8), -2), (dict(I=(1 << 19) + 8), -2), (dict(T=(1 << 26) + 1), -2),
+    (dict(x=None), -1), (dict(w=None), -1), (dict(h=None), -1), (dict(x=X + 8), -1), (dict(w=W + 8), -1),
+    (dict(h=O + 8), -1), (dict(a=A + 8), -1), (dict(a=X), -1), (dict(h=X), -1), (dict(h=A + 128), -1), (dict(h=W + 64), -1),
+])
+def test_glu_refusals(L, bad, want):
+    assert glu(L, **bad) == want
+
+
+def linear_backward(L, dy=D, x=X, w=W, T=4, N=64, K=64, dx=DX, dxt=2, dw=DW, dwt=1, acc=0, ws=S, n=1 << 22):
+    return L.lib.moe_linear_backward(dy, x, w, T, N, K, dx, dxt, dw, dwt, acc, ws, n, None)
+
+
+def glu_backward(L, dh=D, a=A, x=X, w=W, T=4, I=64, K=64, act=3, dx=DX, dxt=2, dw=DW, dwt=1, acc=0, ws=S, n=1 << 22):
+    return L.lib.moe_glu_backward(dh, a, x, w, T, I, K, act, dx, dxt, dw, dwt, acc, ws, n, None)
+
+
+GRAD_BAD = [
+    (dict(T=-1), -1), (dict(K=0), -1), (dict(K=60), -2), (dict(K=(1 << 20) + 8), -2), (dict(T=1 << 30), -2), (dict(dxt=3), -1),
+    (dict(dwt=0), -1), (dict(dx=None, dw=None), -1), (dict(x=None), -1), (dict(w=None), -1), (dict(x=X + 8), -1),
+    (dict(w=W + 2), -1), (dict(dx=DX + 8), -1), (dict(dw=DW + 8), -1), (dict(ws=S + 8), -1), (dict(ws=None), -1),
+    (dict(n=16), -3), (dict(dx=X), -1), (dict(dx=W), -1), (dict(dw=W + 64), -1), (dict(dx=D), -1), (dict(dw=DX + 16), -1),
+    (dict(dw=S), -1), (dict(dx=S + 4096), -1),
+]
+
+
+@pytest.mark.parametrize("bad,want", GRAD_BAD + [(dict(N=0), -1), (dict(N=60), -2), (dict(N=(1 << 20) + 8), -2),
+                                                 (dict(dy=None), -1), (dict(dy=D + 8), -1)])
+def test_linear_backward_refusals(L, bad, want):
+    assert linear_backward(L, **bad) == want
+
+
+@pytest.mark.parametrize("bad,want", GRAD_BAD + [
+    (dict(I=0), -1), (dict(I=60), -2), (dict(I=(1 << 19) + 8), -2), (dict(act=4), -1), (dict(act=-1), -1), (dict(dh=None), -1),
+    (dict(a=None), -1), (dict(dh=D + 8), -1), (dict(a=A + 8), -1), (dict(dw=A), -1), (dict(ws=A), -1), (dict(ws=D), -1)])
+def test_glu_backward_refusals(L, bad, want):
+    assert glu_backward(L, **bad) == want
+
+
+def test_of_no_rows(L):
+    assert quantize(L, rows=0, x=None, q=None, s=None) == 0
+    assert fp8(L, T=0, x=None, xs=None, w=None, ws=None, out=None) == 0
+    assert glu(L, T=0, x=None, w=None, h=None) == 0
+
+
+def test_workspace_sizes(L):
+    for T, N, K in ((0, 8, 8), (1, 64, 64), (4099, 2048, 512)):
+        n = L.lib.moe_linear_backward_ws_bytes(T, N, K)
+        assert n > 0
+        assert linear_backward(L, T=T, N=N, K=K, n=n - 1, ws=at(200), dw=at(400), dx=at(600)) == -3
+        assert L.lib.moe_glu_backward_ws_bytes(T, N // 2 // 8 * 8 or 8, K) >= 4 * T * (N // 2 // 8 * 8)
+    for bad in ((-1, 8, 8), (4, 12, 8), (4, 8, 12), (4, 0, 8), (4, 8, 1 << 21)):
+        assert L.lib.moe_linear_backward_ws_bytes(*bad) == 0
+    for bad in ((-1, 8, 8), (4, 12, 8), (4, 8, 12), (4, 1 << 30, 8)):
+        assert L.lib.moe_glu_backward_ws_bytes(*bad) == 0
+
+
+BF = torch.bfloat16
+
+
+def z(*shape, dtype=BF):
+    return torch.zeros(shape, dtype=dtype)
+
+
+@pytest.mark.parametrize("call", [
+    lambda L: L.moe_fp8_quantize(z(4, 64)),                                   # not on the GPU
+    lambda L: L.moe_fp8_quantize(z(4, 64, dtype=torch.float16)),
+    lambda L: L.moe_fp8_quantize(z(64)),
+    lambda L: L.moe_fp8_quantize(z(4, 64), block_rows=32),
+    lambda L: L.moe_fp8_quantize(z(4, 64), scales=z(4, 2, dtype=torch.float32)),
+    lambda L: L.moe_linear_fp8(z(4, 64, dtype=torch.uint8), z(4, 1, dtype=torch.float32), z(8, 64, dtype=torch.uint8),
+                               z(8, 1, dtype=torch.float32)),                 # a scale per row instead of per block
+    lambda L: L.moe_linear_fp8(z(4, 64, dtype=torch.uint8), z(4, 1, dtype=torch.float32), z(8, 64, dtype=torch.uint8),
+                               z(1, 1, dtype=torch.float32), act="swiglu"),   # gate and up have blocks of their own
+    lambda L: L.moe_linear_fp8(z(4, 64), z(4, 1, dtype=torch.float32), z(8, 64, dtype=torch.uint8),
+                               z(1, 1, dtype=torch.float32)),
+    lambda L: L.moe_linear_fp8(z(4, 64, dtype=torch.uint8), z(4, 1, dtype=torch.float32), z(8, 64, dtype=torch.uint8),
+                               z(1, 1, dtype=torch.float32), act="tanh"),
+    lambda L: L.moe_glu(z(4, 64), z(15, 64)),
+    lambda L: L.moe_glu(z(4, 64), z(16, 64), act="swiglu"),
+    lambda L: L.moe_glu(z(4, 64), z(16, 32)),
+    lambda L: L.moe_glu(z(4, 64), z(16, 64), a=z(4, 8)),
+    lambda L: L.moe_glu(z(4, 128)[:, ::2], z(16, 64)),
+    lambda L: L.moe_linear_backward(z(4, 8), None, z(8, 64)),
+    lambda L: L.moe_linear_backward(z(4, 8), z(4, 64), None),
+    lambda L: L.moe_linear_backward(z(4, 8), z(4, 64), z(8, 64), need_dx=False, need_dw=False),
+    lambda L: L.moe_linear_backward(z(4, 8), z(4, 64), z(8, 64), accumulate=True),
+    lambda L: L.moe_linear_backward(z(4, 8), z(4, 64), z(8, 64), dx=z(4, 64, dtype=torch.float16)),
+    lambda L: L.moe_linear_backward(z(4, 8), z(4, 64), z(8, 64), dw=z(64, 8)),
+    lambda L: L.moe_linear_backward(z(4, 8), z(5, 64), z(8, 64)),
+    lambda L: L.moe_linear_backward(z(4, 8), z(4, 64), z(8, 64), ws=z(4, 4, dtype=torch.uint8)),
+    lambda L: L.moe_glu_backward(z(4, 8), z(4, 8), z(4, 64), z(16, 64)),
+    lambda L: L.moe_glu_backward(z(4, 8), z(4, 16), z(4, 64), z(8, 64)),
+    lambda L: L.moe_glu_backward(z(4, 8), z(4, 16), z(4, 64), z(16, 64), act="swiglu"),
+])
+def test_binding_refusals(L, call):
+    with pytest.raises(ValueError):
+        call(L)
