@@ -59,6 +59,8 @@ struct LinearArgs {
 };
 // few token rows (linear_rows.hip): 16 tt of them to a workgroup, tt = 1, 2 or 4
 hipError_t launch_linear_rows(const LinearArgs& a, LinearKind kind, int tt, hipStream_t s);
+// FP8 with block scales (linear_fp8.hip)
+hipError_t launch_linear_fp8(const LinearArgs& a, hipStream_t s);
 hipError_t launch_linear(const LinearArgs& a, LinearKind kind, hipStream_t s);
 
 // ---- FP8 with a scale per block of 128 (fp8_quant.hip): blocks of by x 128 values, by = 1 or 128

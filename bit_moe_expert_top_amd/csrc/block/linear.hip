@@ -494,7 +494,7 @@ hipError_t launch(const LinearArgs& a, hipStream_t s) {
 
 hipError_t launch_linear(const LinearArgs& a, LinearKind kind, hipStream_t s) {
   const bool gated = a.act == kActSwiglu;
-  if (kind == kFp8) return launch_linear_rows(a, kFp8, a.T <= 16 ? 1 : a.T <= 32 ? 2 : 4, s);
+  if (kind == kFp8) return launch_linear_fp8(a, s);
   if (kind == kMxfp8) return gated ? launch<true, kSwiglu>(a, s) : launch<true, kPlain>(a, s);
   if (a.act == kActGlu) return launch<false, kGlu>(a, s);
   return gated ? launch<false, kSwiglu>(a, s) : launch<false, kPlain>(a, s);
