@@ -15,7 +15,6 @@ constexpr int kMaxE = 1024;
 constexpr int kMaxTopK = 64;
 constexpr int kMaxGroups = 64;
 constexpr int kMaxLinear = 1 << 20;    // N and K
-constexpr int kMaxGradRows = 1 << 20;
 constexpr int kMaxLinearRows = 1 << 26;  // T: a launch has fewer than 2^32 threads
 
 inline hipStream_t as_stream(void* s) { return reinterpret_cast<hipStream_t>(s); }
@@ -38,7 +37,7 @@ inline bool float_dtype(int32_t d) { return d == MOE_DT_F32 || d == MOE_DT_BF16;
 
 // The sizes of a gradient call: rows of 16-byte chunks in all three matrices.
 inline bool grad_sizes(int32_t T, int32_t N, int32_t K) {
-  return T >= 0 && N > 0 && K > 0 && N % 8 == 0 && K % 8 == 0 && N <= kMaxLinear && K <= kMaxLinear && T <= kMaxGradRows;
+  return T >= 0 && N > 0 && K > 0 && N % 8 == 0 && K % 8 == 0 && N <= kMaxLinear && K <= kMaxLinear && T <= kMaxLinearRows;
 }
 inline size_t da_bytes(int64_t T, int64_t I) { return ((size_t)T * I * 4 + 255) / 256 * 256; }
 
@@ -249,8 +248,9 @@ moe_status moe_linear_backward(const uint16_t* dy, const uint16_t* x, const uint
   const Span sdy{dy, (size_t)T * N * 2}, sws{ws, ws_bytes};
   const moe_status bad = grad_args(g, dy, x, w, T, N, K, dx, dx_dtype, dw, dw_dtype, accumulate, sdy, sws);
   if (bad != MOE_OK) return bad;
-  if (ws_bytes < grad_ws_bytes(T, N, K)) return MOE_ERR_WORKSPACE;
-  if (!ws || !aligned(ws, 16)) return MOE_ERR_INVALID_ARG;
+  const size_t need = grad_ws_bytes(T, N, K);
+  if (ws_bytes < need) return MOE_ERR_WORKSPACE;
+  if (need && (!ws || !aligned(ws, 16))) return MOE_ERR_INVALID_ARG;
   return from_hip(launch_grad(g, static_cast<uint8_t*>(ws), as_stream(stream)));
 }
 
@@ -270,8 +270,9 @@ moe_status moe_glu_backward(const uint16_t* dh, const uint16_t* a, const uint16_
   const moe_status bad = grad_args(g, da, x, w, T, 2 * I, K, dx, dx_dtype, dw, dw_dtype, accumulate, sdh, sa, sws);
   if (bad != MOE_OK) return bad;
   if (T > 0 && shares(sws, sdh, sa)) return MOE_ERR_INVALID_ARG;
-  if (ws_bytes < da_bytes(T, I) + grad_ws_bytes(T, 2 * I, K)) return MOE_ERR_WORKSPACE;
-  if (!ws || !aligned(ws, 16)) return MOE_ERR_INVALID_ARG;
+  const size_t need = da_bytes(T, I) + grad_ws_bytes(T, 2 * I, K);
+  if (ws_bytes < need) return MOE_ERR_WORKSPACE;
+  if (need && (!ws || !aligned(ws, 16))) return MOE_ERR_INVALID_ARG;
   if (T > 0) {
     const hipError_t e = launch_glu_grad(dh, a, T, I, act, da, as_stream(stream));
     if (e != hipSuccess) return from_hip(e);

@@ -1,45 +1,16 @@
 // Gradients of a bf16 product y = x W^T and of the gated projection h = act(g) u, [g | u] = x W^T:
 //   dx = dy W (a sum over the weight rows), dW = dy^T x (a sum over the tokens)
 //   dg = dh u act'(g), du = dh act(g), and dy = [dg | du]
-// The sums run along the rows of one operand or of both; the operands are transposed into the workspace and
-// go through the dense product.
 #include <algorithm>
 
 #include "../common.h"
 #include "block_kernels.h"
-#include "linear_dev.h"
 
 namespace bitmoe {
 
 namespace {
 
 constexpr int kThreads = 256;
-
-// src [R][C] -> dst [C][pitch], the columns from R to pitch (R rounded up to 8) zero.  A workgroup moves 64 x 64.
-__global__ __launch_bounds__(kThreads) void transpose_kernel(const uint16_t* src, int R, int C, int pitch, int c_tiles,
-                                                             uint16_t* dst) {
-  __shared__ uint16_t tile[64][66];
-  const int r0 = 64 * (int)(blockIdx.x / c_tiles), c0 = 64 * (int)(blockIdx.x % c_tiles);
-  const int j = threadIdx.x % 64;
-  for (int i = threadIdx.x / 64; i < 64; i += kThreads / 64)
-    tile[i][j] = r0 + i < R && c0 + j < C ? src[(int64_t)(r0 + i) * C + c0 + j] : (uint16_t)0;
-  __syncthreads();
-  for (int i = threadIdx.x / 64; i < 64; i += kThreads / 64)
-    if (c0 + i < C && r0 + j < pitch) dst[(int64_t)(c0 + i) * pitch + r0 + j] = tile[j][i];
-}
-
-hipError_t transpose(const uint16_t* src, int64_t R, int64_t C, uint16_t* dst, hipStream_t s) {
-  const int64_t pitch = (R + 7) / 8 * 8, r_tiles = (pitch + 63) / 64, c_tiles = (C + 63) / 64;
-  transpose_kernel<<<(unsigned)(r_tiles * c_tiles), kThreads, 0, s>>>(src, (int)R, (int)C, (int)pitch, (int)c_tiles, dst);
-  return hipGetLastError();
-}
-
-size_t up256(size_t n) { return (n + 255) / 256 * 256; }
-size_t transposed(int64_t R, int64_t C) { return up256((size_t)C * ((R + 7) / 8 * 8) * 2); }
-
-__global__ __launch_bounds__(kThreads) void fill_kernel(uint32_t* p, int64_t n) {
-  for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < n; i += (int64_t)gridDim.x * kThreads) p[i] = 0;
-}
 
 // act(g) and act'(g) in fp32
 template <int ACT>
@@ -99,48 +70,34 @@ __global__ __launch_bounds__(kThreads) void glu_grad_kernel(const uint16_t* dh, 
   }
 }
 
-hipError_t product(const uint16_t* x, const uint16_t* w, int64_t T, int64_t N, int64_t K, void* out, int out_f32,
-                   bool add, hipStream_t s) {
+// out [T][N] (rows, columns, sums of K) of x and the K-major w
+LinearArgs product(const uint16_t* x, const uint16_t* w, int T, int N, int K, void* out, int out_f32, bool add) {
   LinearArgs a{};
   a.x = reinterpret_cast<const uint8_t*>(x);
   a.w = reinterpret_cast<const uint8_t*>(w);
   a.out = out;
   a.residual = add ? out : nullptr;
-  a.T = (int)T, a.N = a.n_out = (int)N, a.K = (int)K;
-  a.act = kActNone;
+  a.T = T, a.N = a.n_out = N, a.K = K;
   a.res_f32 = a.out_f32 = out_f32;
-  a.vec = N % 4 == 0 && reinterpret_cast<uintptr_t>(out) % (out_f32 ? 16 : 8) == 0;
-  return launch_linear(a, kBf16, s);
+  a.vec = 1;
+  return a;
 }
 
 }  // namespace
 
 size_t grad_ws_bytes(int64_t T, int64_t N, int64_t K) {
-  return transposed(N, K) + transposed(T, N) + transposed(T, K);
+  // one after the other, on the same parts
+  return std::max(grad_product_ws_bytes(T, K, N), grad_product_ws_bytes(N, K, T));
 }
 
 hipError_t launch_grad(const GradArgs& a, uint8_t* ws, hipStream_t s) {
-  const int64_t T = a.T, N = a.N, K = a.K, Tp = (T + 7) / 8 * 8;
-  uint16_t* wt = reinterpret_cast<uint16_t*>(ws);
-  uint16_t* dyt = reinterpret_cast<uint16_t*>(ws + transposed(N, K));
-  uint16_t* xt = reinterpret_cast<uint16_t*>(ws + transposed(N, K) + transposed(T, N));
-  hipError_t e = hipSuccess;
-  if (a.dx && T > 0) {
-    if ((e = transpose(a.w, N, K, wt, s)) != hipSuccess) return e;
-    if ((e = product(a.dy, wt, T, K, N, a.dx, a.dx_f32, false, s)) != hipSuccess) return e;
+  float* parts = reinterpret_cast<float*>(ws);
+  if (a.dx && a.T > 0) {
+    const hipError_t e = launch_grad_product(product(a.dy, a.w, a.T, a.K, a.N, a.dx, a.dx_f32, false), false, parts, s);
+    if (e != hipSuccess) return e;
   }
-  if (a.dw && T > 0) {
-    if ((e = transpose(a.dy, T, N, dyt, s)) != hipSuccess) return e;
-    if ((e = transpose(a.x, T, K, xt, s)) != hipSuccess) return e;
-    return product(dyt, xt, N, K, Tp, a.dw, a.dw_f32, a.accumulate, s);
-  }
-  if (a.dw && !a.accumulate) {
-    const int64_t words = N * K / (a.dw_f32 ? 1 : 2);
-    fill_kernel<<<(unsigned)std::min<int64_t>(1024, (words + kThreads - 1) / kThreads), kThreads, 0, s>>>(
-        static_cast<uint32_t*>(a.dw), words);
-    return hipGetLastError();
-  }
-  return e;
+  if (!a.dw) return hipSuccess;
+  return launch_grad_product(product(a.dy, a.x, a.N, a.K, a.T, a.dw, a.dw_f32, a.accumulate), true, parts, s);
 }
 
 hipError_t launch_glu_grad(const uint16_t* dh, const uint16_t* a, int T, int I, int act, uint16_t* da, hipStream_t s) {

@@ -1,0 +1,400 @@
+// The products behind the gradients, bf16 on v_mfma_f32_32x32x16_bf16 with fp32 sums:
+//   dx = dy W     out[t][k] = sum over n of dy[t][n] w[n][k]     the weights' sum runs along their rows
+//   dW = dy^T x   out[n][k] = sum over t of dy[t][n] x[t][k]     both operands' sums run along their rows
+// In the terms of moe_linear: out [T][N] = x W^T, where an operand that is stored [K][rows] ("K-major") is transposed on
+// its way from LDS into the registers: ds_read_b64_tr_b16 gives lane i of 16 the i-th value of each of four rows of 16, of
+// which every lane points at four values; two of them make a lane's 8 k of one row of the operand.
+//
+// Stages of 64 k in LDS, filled by direct global -> LDS loads: a row-major operand as rows of 128 bytes, its 16-byte chunks
+// XOR-swizzled by row / 2 as in moe_linear; a K-major one as 64 rows of its BM (or BN) values.  There a half wave reads 64
+// bytes of each of four rows, and these lie in different quarters of the banks where the chunks are XOR-swizzled by 4 (k % 4)
+// (rows of 256 bytes and more) or 4 (k / 2 % 2) (128 bytes).
+// A step loads and waits without a branch: past the last k it loads zeros.  The rest is moe_linear's: the weight tile is the
+// MFMA's A operand, operands are read one sub-step of 16 k ahead, the sums pass through LDS in the epilogue.
+#include <algorithm>
+#include <type_traits>
+
+#include "linear_dev.h"
+
+namespace bitmoe {
+
+namespace {
+
+constexpr int kXcds = 8;
+constexpr int kStepK = 64, kSub = kStepK / 16;  // k of a stage, MFMA sub-steps
+
+typedef short i16x4 __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) i16x4 lds_i16x4;
+
+// LDS offsets of a stage are below 2^16
+__device__ __forceinline__ u32x4 read_tr(const uint8_t* p0, const uint8_t* p1) {
+  const u32x2 a = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4*)p0));
+  const u32x2 b = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4*)p1));
+  return u32x4{a[0], a[1], b[0], b[1]};
+}
+
+// Where a wave's direct loads of one operand (BR rows of it in the tile, NW waves) come from and go to.
+template <bool KM, int BR, int NW>
+struct Source {
+  static constexpr int kLoads = BR * 128 / 1024 / NW;  // of a wave and stage
+  static constexpr int kPitch = KM ? 2 * BR : 128, kRows = 1024 / kPitch, kChunks = kPitch / 16;
+  static_assert(BR * 128 % (1024 * NW) == 0, "loads");
+  uint32_t off[kLoads];
+  uint32_t chunk;  // row-major: the lane's chunk of a row
+  const uint8_t* base;
+  int64_t ld;      // bytes from row to row as stored
+  int rows;        // row-major: rows of the operand in the tile
+  __device__ static int swizzle(int row) { return KM ? (BR >= 128 ? 4 * (row & 3) : 4 * (row >> 1 & 1)) : row >> 1 & 7; }
+  // row0: the tile's first row of the operand, of `total`; K: length of the sum
+  __device__ void init(const uint8_t* p, int64_t row0, int64_t total, int K, int w, int lane) {
+    const int r0 = lane / kChunks, c = lane % kChunks;
+    rows = (int)min((int64_t)BR, total - row0);
+    ld = 2 * (KM ? total : (int64_t)K);
+    base = KM ? p + 2 * row0 : p + row0 * ld;
+    chunk = 16u * (uint32_t)(c ^ swizzle(kRows * w + r0));
+#pragma unroll
+    for (int u = 0; u < kLoads; ++u) {
+      const int r = kRows * (NW * u + w) + r0;
+      off[u] = !KM && r >= rows ? kOffNone : (uint32_t)(r * ld) + 16u * (uint32_t)(c ^ swizzle(r));
+    }
+  }
+  // load u of the stage that starts at k0 (K, the sum's end, lies within 64 rows of a K-major operand's resource)
+  __device__ void load(uint8_t* stage, int u, int64_t k0, int64_t K, int64_t total, int64_t row0, int w) const {
+    lds_void* dst = (lds_void*)(stage + 1024 * (NW * u + w));
+    if constexpr (KM) {
+      const int left = (int)max((int64_t)0, min((int64_t)kStepK, K - k0));
+      const buf_rsrc r = make_rsrc(base + k0 * ld, (uint32_t)max(left * (int)ld - (int)(2 * row0), 0));
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(r, dst, 16, (int)off[u], 0, 0, 0);
+    } else {
+      const buf_rsrc r = make_rsrc(base, (uint32_t)(rows * ld));
+      const bool in = 2 * k0 + (int64_t)chunk < 2 * K;
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(r, dst, 16, (int)(in ? off[u] : kOffNone), (int)(2 * k0), 0, 0);
+    }
+  }
+};
+
+// A lane's reads of one operand's 32-row tiles i0 .. i0 + N - 1.
+template <bool KM, int BR, int N>
+struct Reader {
+  uint32_t at[KM ? N : kSub];
+  uint32_t first;
+  __device__ void init(int i0, int lane) {
+    const int r32 = lane & 31, hl = lane >> 5;
+    if constexpr (KM) {
+      // 16 lanes point at four k rows (lane / 4 % 4) of 16 values each
+      const int k4 = lane >> 2 & 3, k = 8 * hl + k4;
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        const int v = 32 * (i0 + i) + 16 * (lane >> 4 & 1) + 4 * (lane & 3);  // value of the row
+        at[i] = (uint32_t)(k * 2 * BR) + 16u * (uint32_t)(v / 8 ^ Source<KM, BR, 1>::swizzle(k4)) + 2u * (uint32_t)(v % 8);
+      }
+      first = 0;
+    } else {
+#pragma unroll
+      for (int j = 0; j < kSub; ++j) at[j] = 16u * (uint32_t)((2 * j + hl) ^ Source<KM, BR, 1>::swizzle(r32));
+      first = (uint32_t)(32 * i0 + r32) * 128;
+    }
+  }
+  __device__ u32x4 read(const uint8_t* stage, int j, int i) const {
+    if constexpr (KM) {
+      const uint8_t* p = stage + at[i] + 16 * j * 2 * BR;
+      return read_tr(p, p + 4 * 2 * BR);
+    } else {
+      return *reinterpret_cast<const u32x4*>(stage + first + at[j] + 32 * 128 * i);
+    }
+  }
+};
+
+// x: T rows, w: N rows, sums of K; w is K-major, x is if XT.  The sums of split blockIdx / tiles, of `per` steps each, go to
+// out + split * T * N (fp32 parts, where there are several).
+template <bool XT, int BM, int BN, int WM, int WN, int S, int kSpread>
+__global__ __launch_bounds__(64 * WM * WN, 2) void grad_tile_kernel(LinearArgs a, int m_tiles, int n_tiles, int per) {
+  a.act = kActNone;  // known to the compiler
+  constexpr int NW = WM * WN;
+  constexpr int AT = BM / WM / 32, BT = BN / WN / 32;  // token and weight MFMA tiles of a wave
+  typedef Source<XT, BM, NW> SX;
+  typedef Source<true, BN, NW> SW;
+  constexpr int UA = SX::kLoads, UB = SW::kLoads, LD = UA + UB, kStage = (BM + BN) * 128;
+  static_assert((S == 2 || S == 4) && kSpread <= kSub && LD % kSpread == 0, "ring");
+  // one object per stage: the compiler tracks direct loads per object
+  __shared__ __align__(16) uint8_t st0[kStage], st1[kStage], st2[S == 4 ? kStage : 16], st3[S == 4 ? kStage : 16];
+  const int tid = threadIdx.x, lane = wave_lane(), r32 = lane & 31, hl = lane >> 5;
+  const int w = __builtin_amdgcn_readfirstlane(tid / kWave), wm = w % WM, wn = w / WM;
+
+  // Workgroups go to the 8 XCDs round robin.  Each XCD takes a contiguous run of tiles, ordered in bands of 8 token
+  // tiles, column by column, so that the tiles running on it at a time share their rows and columns in its L2.
+  const int total = m_tiles * n_tiles, split = blockIdx.x / total;
+  int tile;
+  {
+    const int b = blockIdx.x - split * total, each = total / kXcds, rest = total % kXcds;
+    const int x = b % kXcds, i = b / kXcds;
+    tile = x * each + min(x, rest) + i;
+  }
+  constexpr int kBand = 8;
+  const int band = tile / (kBand * n_tiles), in_band = tile - band * kBand * n_tiles;
+  const int band_rows = min(kBand, m_tiles - band * kBand);
+  const int64_t t0 = (int64_t)(band * kBand + in_band % band_rows) * BM;
+  const int n0 = in_band / band_rows * BN;  // first output column
+  const int64_t k_first = (int64_t)split * per * kStepK, k_end = min((int64_t)a.K, k_first + (int64_t)per * kStepK);
+  const int nk = (int)((k_end - k_first + kStepK - 1) / kStepK);
+
+  SX sx;
+  SW sw;
+  sx.init(a.x, t0, a.T, a.K, w, lane);
+  sw.init(a.w, n0, a.N, a.K, w, lane);
+  Reader<XT, BM, AT> rx;
+  Reader<true, BN, BT> rw;
+  rx.init(AT * wm, lane);
+  rw.init(BT * wn, lane);
+  // the stage buffers by index (a constant wherever they are used)
+  auto stage = [&](int d) -> uint8_t* { return d == 0 ? st0 : d == 1 ? st1 : d == 2 ? st2 : st3; };
+  // direct load i of stage kb into buffer d: the token operand's, then the weights'
+  auto load_one = [&](int d, int kb, int i) {
+    const int64_t k0 = k_first + (int64_t)kb * kStepK;
+    if (i < UA)
+      sx.load(stage(d), i, k0, k_end, a.T, t0, w);
+    else
+      sw.load(stage(d) + BM * 128, i - UA, k0, k_end, a.N, n0, w);
+  };
+  struct Ops {
+    u32x4 x[AT], w[BT];
+  } op[2];
+  f32x16_t acc[AT][BT];
+#pragma unroll
+  for (int t = 0; t < AT; ++t)
+#pragma unroll
+    for (int b = 0; b < BT; ++b)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) acc[t][b][i] = 0.f;
+  auto read_w = [&](Ops& o, int d, int j, int b) { o.w[b] = rw.read(stage(d) + BM * 128, j, b); };
+  auto read_x = [&](Ops& o, int d, int j, int t) { o.x[t] = rx.read(stage(d), j, t); };
+
+#pragma unroll
+  for (int d = 0; d < S; ++d)
+#pragma unroll
+    for (int i = 0; i < LD; ++i)
+      if (d < S - 1 || i < LD / kSpread) load_one(d, d, i);
+  wait_vm<(S - 2) * LD + LD / kSpread, false>();
+  asm volatile("s_barrier" ::: "memory");
+#pragma unroll
+  for (int b = 0; b < BT; ++b) read_w(op[0], 0, 0, b);
+#pragma unroll
+  for (int t = 0; t < AT; ++t) read_x(op[0], 0, 0, t);
+
+  // Step kb, its stage in buffer I and in LDS for all waves, its first operands in op[0].
+  auto step = [&](auto I_, int kb) {
+    constexpr int d = decltype(I_)::value, next = (d + 1) % S;
+#pragma unroll
+    for (int j = 0; j < kSub; ++j) {
+      const bool last = j == kSub - 1;
+      // part p of a refill: 0 in the last sub-step of the step that read the buffer, the others in the first sub-steps of the
+      // next step
+      const int p = last ? 0 : j + 1, fd = last ? d : (d + S - 1) % S, fk = last ? kb + S : kb - 1 + S;
+      if (last) {
+        // this wave's loads of the next stage have landed (those of later ones may be in flight) and it has read this stage
+        wait_vm<(S - 2) * LD, true>();
+        asm volatile("s_barrier" ::: "memory");
+      }
+#pragma unroll
+      for (int t = 0; t < AT; ++t) {
+        // a share of the next sub-step's operands, the weight tiles first (all MFMAs of a token tile need them)
+#pragma unroll
+        for (int i = 0; i < BT + AT; ++i) {
+          constexpr int kShare = (BT + AT + AT - 1) / AT + (AT > 2 ? 1 : 0);
+          if (i / kShare != t && !(t == AT - 1 && i / kShare > t)) continue;
+          if (i < BT)
+            read_w(op[(j + 1) & 1], last ? next : d, last ? 0 : j + 1, i < BT ? i : 0);
+          else
+            read_x(op[(j + 1) & 1], last ? next : d, last ? 0 : j + 1, i < BT ? 0 : i - BT);
+        }
+        if (p < kSpread) {
+#pragma unroll
+          for (int i = 0; i < LD; ++i)
+            if (i * AT * kSpread / LD == p * AT + t) load_one(fd, fk, i);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int b = 0; b < BT; ++b) acc[t][b] = mfma_bf16_32x32x16(op[j & 1].w[b], op[j & 1].x[t], acc[t][b]);
+        if constexpr (AT * BT == 8) {  // held to issue here, in the ordinary registers
+#pragma unroll
+          for (int b = 0; b < BT; ++b) hold(acc[t][b]);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    }
+  };
+  using I0 = std::integral_constant<int, 0>;
+  using I1 = std::integral_constant<int, 1>;
+  using I2 = std::integral_constant<int, 2>;
+  using I3 = std::integral_constant<int, 3>;
+  int kb = 0;
+  // no way out but the loop's end: the compiler would wait at its head for what any of the ways leaves in flight
+  for (; kb + S <= nk; kb += S) {
+    step(I0{}, kb);
+    step(I1{}, kb + 1);
+    if constexpr (S == 4) {
+      step(I2{}, kb + 2);
+      step(I3{}, kb + 3);
+    }
+  }
+  if (kb < nk) step(I0{}, kb);
+  if constexpr (S == 4) {
+    if (kb + 1 < nk) step(I1{}, kb + 1);
+    if (kb + 2 < nk) step(I2{}, kb + 2);
+  }
+  wait_vm<0, true>();
+
+  // ---- epilogue: 32 token rows of the wave at a time pass through the wave's part of the stages (rows of 32 BT sums and a
+  // pad of four), then a lane takes four consecutive columns.  What is added to is fetched before the turn's stores.
+  constexpr int kPitch = 32 * BT + 4, kCols = 32 * BT, kLanes = kCols / 4;
+  constexpr int kStep = kWave / kLanes, kStores = 32 / kStep;  // rows of a store, stores of a turn
+  const int ec = 4 * (lane % kLanes), n = n0 + kCols * wn + ec, er = lane / kLanes;
+  const int64_t row0 = t0 + 32 * AT * wm + er;  // this lane's first row
+  const int rows = n < a.n_out ? (int)max((int64_t)0, min((int64_t)32 * AT, a.T - (row0 - er))) - er : 0;
+  const int64_t at0 = row0 * a.n_out + n;
+  if (split > 0) a.out = reinterpret_cast<float*>(a.out) + (int64_t)split * a.T * a.n_out;
+  const FourBias none{};
+  Four res[kStores];
+  auto fetch = [&](int t) {
+    if (a.residual) {
+#pragma unroll
+      for (int i = 0; i < kStores; ++i)
+        if (32 * t + i * kStep < rows) res[i] = load_residual4(a, at0 + (int64_t)(32 * t + i * kStep) * a.n_out, n);
+    }
+  };
+  fetch(0);
+  __syncthreads();  // all waves have read the last stage
+  constexpr int kFit = kStage / (32 * kPitch * 4);  // waves whose part fits one stage
+  static_assert(kFit > 0 && (NW + kFit - 1) / kFit <= S, "epilogue staging");
+  float* ep = reinterpret_cast<float*>(stage(w / kFit)) + w % kFit * 32 * kPitch;
+  const float* get = ep + er * kPitch + ec;
+  // the loop is not unrolled, for the size of its code; the sums are picked with constant indexes
+#pragma unroll 1
+  for (int t = 0; t < AT; ++t) {
+#pragma unroll
+    for (int i = 0; i < AT; ++i)
+      if (t == i) {
+#pragma unroll
+        for (int b = 0; b < BT; ++b)
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            *reinterpret_cast<float4*>(ep + r32 * kPitch + 32 * b + 8 * q + 4 * hl) =
+                make_float4(acc[i][b][4 * q], acc[i][b][4 * q + 1], acc[i][b][4 * q + 2], acc[i][b][4 * q + 3]);
+      }
+    __builtin_amdgcn_wave_barrier();
+    Four now[kStores];
+#pragma unroll
+    for (int i = 0; i < kStores; ++i) now[i] = res[i];
+    if (t + 1 < AT) fetch(t + 1);
+#pragma unroll
+    for (int i = 0; i < kStores; ++i) {
+      const float4 v4 = *reinterpret_cast<const float4*>(get + i * kStep * kPitch);
+      const float v[4] = {v4.x, v4.y, v4.z, v4.w};
+      if (32 * t + i * kStep < rows)
+        epilogue4<kPlain, (BM * BN > 64 * 64)>(a, at0 + (int64_t)(32 * t + i * kStep) * a.n_out, n, v, v, none, now[i]);
+    }
+    __builtin_amdgcn_wave_barrier();
+  }
+}
+
+// out = the sum of the splits' parts [splits][n], in their order, added to what out holds if add; four values a thread.
+template <typename OT>
+__global__ __launch_bounds__(256) void join_kernel(const float* parts, int splits, int64_t n, OT* out, int add) {
+  for (int64_t i = 4 * ((int64_t)blockIdx.x * 256 + threadIdx.x); i < n; i += (int64_t)gridDim.x * 1024) {
+    f32x4 v = *reinterpret_cast<const f32x4*>(parts + i);
+    for (int s = 1; s < splits; ++s) v += *reinterpret_cast<const f32x4*>(parts + s * n + i);
+    if constexpr (sizeof(OT) == 4) {
+      f32x4* o = reinterpret_cast<f32x4*>(out + i);
+      *o = add ? v + *o : v;
+    } else {
+      u32x2* o = reinterpret_cast<u32x2*>(out + i);
+      if (add) {
+        const u32x2 q = *o;
+        v += f32x4{__uint_as_float(q[0] << 16), __uint_as_float(q[0] & 0xFFFF0000u), __uint_as_float(q[1] << 16),
+                   __uint_as_float(q[1] & 0xFFFF0000u)};
+      }
+      *o = u32x2{f32x2_to_bf16x2_rne(v[0], v[1]), f32x2_to_bf16x2_rne(v[2], v[3])};
+    }
+  }
+}
+
+// Which tiles, and over how many splits of the sum: what takes the least time by this model.  A round is the workgroups that
+// run at once; it takes base + slope per 1024 of the sum's length (us, measured on sums of 1024, 2048 and 4096 over full
+// rounds):
+//   rows x columns                           at once    base   slope
+//   64 x 64, four stages                     256        6      2.8
+//   64 x 64, four stages                     512        5.5    6
+//   128 x 128, eight waves, four stages      256        7      7.8
+//   256 x 128, eight waves, two stages       256        8      14.5
+//   256 x 256, eight waves, two stages       256        12.5   23.6
+// (128 x 128 by four waves, two workgroups to a CU: 8 and 15 for 512, never the least.)  The parts of several splits are
+// written and read once more in fp32, at about 5 TB/s and 4 us for the launch.
+enum Variant { kTile64, kTile128, kTile256x128, kTile256 };
+struct Plan {
+  Variant tiles;
+  int splits, per;  // steps of a split
+};
+Plan choose(int64_t T, int64_t N, int64_t K) {
+  Plan best{kTile64, 1, 0};
+  double least = 1e30;
+  const int64_t steps = (K + kStepK - 1) / kStepK;
+  auto consider = [&](Variant v, int bm, int bn, int at_once, double base, double slope) {
+    const int64_t n = ((T + bm - 1) / bm) * ((N + bn - 1) / bn);
+    for (int s = 1; s <= 16; s *= 2) {
+      const int64_t per = std::max<int64_t>((steps + s - 1) / s, 1), splits = std::max<int64_t>((steps + per - 1) / per, 1);
+      if (s > 1 && (per < 4 || n * splits > 512)) break;
+      const double rounds = (double)((n * splits + at_once - 1) / at_once);
+      const double t = rounds * (base + slope * (double)per / 16) + (splits > 1 ? 4 + 8e-6 * T * N * splits / 5 : 0.0);
+      if (t < least) least = t, best = {v, (int)splits, (int)per};
+    }
+  };
+  consider(kTile64, 64, 64, 256, 6.0, 2.8);
+  consider(kTile64, 64, 64, 512, 5.5, 6.0);
+  consider(kTile128, 128, 128, 256, 7.0, 7.8);
+  consider(kTile256x128, 256, 128, 256, 8.0, 14.5);
+  consider(kTile256, 256, 256, 256, 12.5, 23.6);
+  return best;
+}
+
+template <bool XT, int BM, int BN, int WM, int WN, int S, int kSpread>
+hipError_t go(const LinearArgs& a, const Plan& p, hipStream_t s) {
+  const int m_tiles = (a.T + BM - 1) / BM, n_tiles = (a.N + BN - 1) / BN;
+  grad_tile_kernel<XT, BM, BN, WM, WN, S, kSpread>
+      <<<(unsigned)((int64_t)m_tiles * n_tiles * p.splits), 64 * WM * WN, 0, s>>>(a, m_tiles, n_tiles, p.per);
+  return hipGetLastError();
+}
+
+template <bool XT>
+hipError_t launch(const LinearArgs& a, const Plan& p, hipStream_t s) {
+  if (p.tiles == kTile64) return go<XT, 64, 64, 2, 2, 4, 1>(a, p, s);
+  if (p.tiles == kTile128) return go<XT, 128, 128, 4, 2, 4, 2>(a, p, s);
+  if (p.tiles == kTile256x128) return go<XT, 256, 128, 4, 2, 2, 1>(a, p, s);
+  return go<XT, 256, 256, 2, 4, 2, 2>(a, p, s);
+}
+
+}  // namespace
+
+size_t grad_product_ws_bytes(int64_t T, int64_t N, int64_t K) {
+  const Plan p = choose(T, N, K);
+  return p.splits > 1 ? (size_t)p.splits * T * N * 4 : 0;
+}
+
+hipError_t launch_grad_product(const LinearArgs& a, bool x_k_major, float* parts, hipStream_t s) {
+  const Plan p = choose(a.T, a.N, a.K);
+  if (p.splits == 1) return x_k_major ? launch<true>(a, p, s) : launch<false>(a, p, s);
+  LinearArgs part = a;
+  part.out = parts;
+  part.residual = nullptr;
+  part.out_f32 = 1;
+  const hipError_t e = x_k_major ? launch<true>(part, p, s) : launch<false>(part, p, s);
+  if (e != hipSuccess) return e;
+  const int64_t n = (int64_t)a.T * a.N;
+  const unsigned grid = (unsigned)std::min<int64_t>((n / 4 + 255) / 256, 1 << 16);
+  if (a.out_f32)
+    join_kernel<<<grid, 256, 0, s>>>(parts, p.splits, n, static_cast<float*>(a.out), a.residual != nullptr);
+  else
+    join_kernel<<<grid, 256, 0, s>>>(parts, p.splits, n, static_cast<uint16_t*>(a.out), a.residual != nullptr);
+  return hipGetLastError();
+}
+
+}  // namespace bitmoe

@@ -488,12 +488,13 @@ moe_status moe_glu(const uint16_t* x, const uint16_t* w, int32_t T, int32_t I, i
  *   dy bf16 [T][N], x bf16 [T][K], w bf16 [N][K]
  *   dx    [T][K] of dx_dtype (F32 or BF16), or NULL (then w may be NULL)
  *   dw    [N][K] of dw_dtype (F32 or BF16), or NULL (then x may be NULL); not both NULL
- *   ws    moe_linear_backward_ws_bytes(T, N, K) bytes, 16-byte aligned
+ *   ws    moe_linear_backward_ws_bytes(T, N, K) bytes, 16-byte aligned (fp32 parts of long sums of few outputs; NULL where
+ *         it is 0)
  * Sums are fp32 on the matrix cores, rounded once; the same call gives the same bits.  T = 0 leaves dw zero (or, with
  * accumulate, as it is).  No output may overlap an input, the other output or the workspace.
- * moe_linear_backward_ws_bytes returns 0 for sizes that the call refuses.
+ * The order of a row's sums may follow the sizes.  moe_linear_backward_ws_bytes is 0 also for sizes that the call refuses.
  * Errors: INVALID_ARG (bad sizes, types or pointers; a pointer not 16-byte aligned; overlaps), WORKSPACE (ws_bytes too
- * small), UNSUPPORTED (N or K % 8 != 0, N or K > 2^20, T > 2^20). */
+ * small), UNSUPPORTED (N or K % 8 != 0, N or K > 2^20, T > 2^26). */
 size_t moe_linear_backward_ws_bytes(int32_t T, int32_t N, int32_t K);
 moe_status moe_linear_backward(const uint16_t* dy, const uint16_t* x, const uint16_t* w, int32_t T, int32_t N, int32_t K,
                                void* dx, int32_t dx_dtype, void* dw, int32_t dw_dtype, int32_t accumulate, void* ws,

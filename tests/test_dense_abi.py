@@ -72,8 +72,7 @@ def glu_backward(L, dh=D, a=A, x=X, w=W, T=4, I=64, K=64, act=3, dx=DX, dxt=2, d
 GRAD_BAD = [
     (dict(T=-1), -1), (dict(K=0), -1), (dict(K=60), -2), (dict(K=(1 << 20) + 8), -2), (dict(T=1 << 30), -2), (dict(dxt=3), -1),
     (dict(dwt=0), -1), (dict(dx=None, dw=None), -1), (dict(x=None), -1), (dict(w=None), -1), (dict(x=X + 8), -1),
-    (dict(w=W + 2), -1), (dict(dx=DX + 8), -1), (dict(dw=DW + 8), -1), (dict(ws=S + 8), -1), (dict(ws=None), -1),
-    (dict(n=16), -3), (dict(dx=X), -1), (dict(dx=W), -1), (dict(dw=W + 64), -1), (dict(dx=D), -1), (dict(dw=DX + 16), -1),
+    (dict(w=W + 2), -1), (dict(dx=DX + 8), -1), (dict(dw=DW + 8), -1), (dict(dx=X), -1), (dict(dx=W), -1), (dict(dw=W + 64), -1), (dict(dx=D), -1), (dict(dw=DX + 16), -1),
     (dict(dw=S), -1), (dict(dx=S + 4096), -1),
 ]
 
@@ -86,7 +85,8 @@ def test_linear_backward_refusals(L, bad, want):
 
 @pytest.mark.parametrize("bad,want", GRAD_BAD + [
     (dict(I=0), -1), (dict(I=60), -2), (dict(I=(1 << 19) + 8), -2), (dict(act=4), -1), (dict(act=-1), -1), (dict(dh=None), -1),
-    (dict(a=None), -1), (dict(dh=D + 8), -1), (dict(a=A + 8), -1), (dict(dw=A), -1), (dict(ws=A), -1), (dict(ws=D), -1)])
+    (dict(a=None), -1), (dict(dh=D + 8), -1), (dict(a=A + 8), -1), (dict(dw=A), -1), (dict(ws=A), -1), (dict(ws=D), -1),
+    (dict(ws=S + 8), -1), (dict(ws=None), -1), (dict(n=16), -3)])
 def test_glu_backward_refusals(L, bad, want):
     assert glu_backward(L, **bad) == want
 
@@ -98,11 +98,18 @@ def test_of_no_rows(L):
 
 
 def test_workspace_sizes(L):
-    for T, N, K in ((0, 8, 8), (1, 64, 64), (4099, 2048, 512)):
-        n = L.lib.moe_linear_backward_ws_bytes(T, N, K)
-        assert n > 0
-        assert linear_backward(L, T=T, N=N, K=K, n=n - 1, ws=at(200), dw=at(400), dx=at(600)) == -3
-        assert L.lib.moe_glu_backward_ws_bytes(T, N // 2 // 8 * 8 or 8, K) >= 4 * T * (N // 2 // 8 * 8)
+    """A byte less than the call needs is refused; long sums of few outputs are split and need one, whole tiles do not."""
+    n = L.lib.moe_linear_backward_ws_bytes(16384, 512, 256)
+    assert n > 0 and L.lib.moe_linear_backward_ws_bytes(8192, 4096, 4096) == 0
+    far = dict(dy=at(100), x=at(200), w=at(300), dx=at(400), dw=at(500), ws=at(600))
+    assert linear_backward(L, T=16384, N=512, K=256, n=n - 1, **far) == -3
+    assert linear_backward(L, T=16384, N=512, K=256, n=n, **{**far, "ws": at(600) + 8}) == -1
+    for T, I, K in ((1, 64, 64), (4099, 1024, 512), (16384, 256, 256)):
+        n = L.lib.moe_glu_backward_ws_bytes(T, I, K)
+        assert n >= 4 * T * I + L.lib.moe_linear_backward_ws_bytes(T, 2 * I, K)
+        assert glu_backward(L, T=T, I=I, K=K, n=n - 1, dh=at(100), x=at(200), w=at(300), dx=at(400), dw=at(500), ws=at(600),
+                            a=at(700)) == -3
+    assert L.lib.moe_glu_backward_ws_bytes(0, 64, 64) == 0
     for bad in ((-1, 8, 8), (4, 12, 8), (4, 8, 12), (4, 0, 8), (4, 8, 1 << 21)):
         assert L.lib.moe_linear_backward_ws_bytes(*bad) == 0
     for bad in ((-1, 8, 8), (4, 12, 8), (4, 8, 12), (4, 1 << 30, 8)):
