@@ -80,7 +80,7 @@ struct GradArgs {
 };
 // The products behind them (grad_tile.hip): out [T][N] = x W^T with w K-major ([K][N]) and x K-major or not; of a, what
 // moe_linear's epilogue needs for act none; a residual is out itself.  parts: grad_product_ws_bytes bytes.
-size_t grad_product_ws_bytes(int64_t T, int64_t N, int64_t K);
+size_t grad_product_ws_bytes(int64_t T, int64_t N, int64_t K, bool x_k_major);
 hipError_t launch_grad_product(const LinearArgs& a, bool x_k_major, float* parts, hipStream_t s);
 size_t grad_ws_bytes(int64_t T, int64_t N, int64_t K);
 hipError_t launch_grad(const GradArgs& a, uint8_t* ws, hipStream_t s);

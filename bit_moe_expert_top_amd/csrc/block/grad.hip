@@ -87,7 +87,7 @@ LinearArgs product(const uint16_t* x, const uint16_t* w, int T, int N, int K, vo
 
 size_t grad_ws_bytes(int64_t T, int64_t N, int64_t K) {
   // one after the other, on the same parts
-  return std::max(grad_product_ws_bytes(T, K, N), grad_product_ws_bytes(N, K, T));
+  return std::max(grad_product_ws_bytes(T, K, N, false), grad_product_ws_bytes(N, K, T, true));
 }
 
 hipError_t launch_grad(const GradArgs& a, uint8_t* ws, hipStream_t s) {

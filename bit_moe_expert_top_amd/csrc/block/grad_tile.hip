@@ -5,7 +5,7 @@
 // its way from LDS into the registers: ds_read_b64_tr_b16 gives lane i of 16 the i-th value of each of four rows of 16, of
 // which every lane points at four values; two of them make a lane's 8 k of one row of the operand.
 //
-// Stages of 64 k in LDS, filled by direct global -> LDS loads: a row-major operand as rows of 128 bytes, its 16-byte chunks
+// Stages of SK (64 or 32) k in LDS, filled by direct global -> LDS loads: a row-major operand as rows of 128 bytes, its 16-byte chunks
 // XOR-swizzled by row / 2 as in moe_linear; a K-major one as 64 rows of its BM (or BN) values.  There a half wave reads 64
 // bytes of each of four rows, and these lie in different quarters of the banks where the chunks are XOR-swizzled by 4 (k % 4)
 // (rows of 256 bytes and more) or 4 (k / 2 % 2) (128 bytes).
@@ -21,7 +21,6 @@ namespace bitmoe {
 namespace {
 
 constexpr int kXcds = 8;
-constexpr int kStepK = 64, kSub = kStepK / 16;  // k of a stage, MFMA sub-steps
 
 typedef short i16x4 __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) i16x4 lds_i16x4;
@@ -34,17 +33,17 @@ __device__ __forceinline__ u32x4 read_tr(const uint8_t* p0, const uint8_t* p1) {
 }
 
 // Where a wave's direct loads of one operand (BR rows of it in the tile, NW waves) come from and go to.
-template <bool KM, int BR, int NW>
+template <bool KM, int BR, int NW, int SK>
 struct Source {
-  static constexpr int kLoads = BR * 128 / 1024 / NW;  // of a wave and stage
-  static constexpr int kPitch = KM ? 2 * BR : 128, kRows = 1024 / kPitch, kChunks = kPitch / 16;
-  static_assert(BR * 128 % (1024 * NW) == 0, "loads");
+  static constexpr int kLoads = BR * 2 * SK / 1024 / NW;  // of a wave and stage
+  static constexpr int kPitch = KM ? 2 * BR : 2 * SK, kRows = 1024 / kPitch, kChunks = kPitch / 16;
+  static_assert(BR * 2 * SK % (1024 * NW) == 0, "loads");
   uint32_t off[kLoads];
   uint32_t chunk;  // row-major: the lane's chunk of a row
   const uint8_t* base;
   int64_t ld;      // bytes from row to row as stored
   int rows;        // row-major: rows of the operand in the tile
-  __device__ static int swizzle(int row) { return KM ? (BR >= 128 ? 4 * (row & 3) : 4 * (row >> 1 & 1)) : row >> 1 & 7; }
+  __device__ static int swizzle(int row) { return KM ? (BR >= 128 ? 4 * (row & 3) : 4 * (row >> 1 & 1)) : SK == 64 ? row >> 1 & 7 : row >> 2 & 3; }
   // row0: the tile's first row of the operand, of `total`; K: length of the sum
   __device__ void init(const uint8_t* p, int64_t row0, int64_t total, int K, int w, int lane) {
     const int r0 = lane / kChunks, c = lane % kChunks;
@@ -62,7 +61,7 @@ struct Source {
   __device__ void load(uint8_t* stage, int u, int64_t k0, int64_t K, int64_t total, int64_t row0, int w) const {
     lds_void* dst = (lds_void*)(stage + 1024 * (NW * u + w));
     if constexpr (KM) {
-      const int left = (int)max((int64_t)0, min((int64_t)kStepK, K - k0));
+      const int left = (int)max((int64_t)0, min((int64_t)SK, K - k0));
       const buf_rsrc r = make_rsrc(base + k0 * ld, (uint32_t)max(left * (int)ld - (int)(2 * row0), 0));
       __builtin_amdgcn_raw_ptr_buffer_load_lds(r, dst, 16, (int)off[u], 0, 0, 0);
     } else {
@@ -74,9 +73,9 @@ struct Source {
 };
 
 // A lane's reads of one operand's 32-row tiles i0 .. i0 + N - 1.
-template <bool KM, int BR, int N>
+template <bool KM, int BR, int N, int SK>
 struct Reader {
-  uint32_t at[KM ? N : kSub];
+  uint32_t at[KM ? N : SK / 16];
   uint32_t first;
   __device__ void init(int i0, int lane) {
     const int r32 = lane & 31, hl = lane >> 5;
@@ -86,13 +85,13 @@ struct Reader {
 #pragma unroll
       for (int i = 0; i < N; ++i) {
         const int v = 32 * (i0 + i) + 16 * (lane >> 4 & 1) + 4 * (lane & 3);  // value of the row
-        at[i] = (uint32_t)(k * 2 * BR) + 16u * (uint32_t)(v / 8 ^ Source<KM, BR, 1>::swizzle(k4)) + 2u * (uint32_t)(v % 8);
+        at[i] = (uint32_t)(k * 2 * BR) + 16u * (uint32_t)(v / 8 ^ Source<KM, BR, 1, SK>::swizzle(k4)) + 2u * (uint32_t)(v % 8);
       }
       first = 0;
     } else {
 #pragma unroll
-      for (int j = 0; j < kSub; ++j) at[j] = 16u * (uint32_t)((2 * j + hl) ^ Source<KM, BR, 1>::swizzle(r32));
-      first = (uint32_t)(32 * i0 + r32) * 128;
+      for (int j = 0; j < SK / 16; ++j) at[j] = 16u * (uint32_t)((2 * j + hl) ^ Source<KM, BR, 1, SK>::swizzle(r32));
+      first = (uint32_t)(32 * i0 + r32) * 2 * SK;
     }
   }
   __device__ u32x4 read(const uint8_t* stage, int j, int i) const {
@@ -100,21 +99,22 @@ struct Reader {
       const uint8_t* p = stage + at[i] + 16 * j * 2 * BR;
       return read_tr(p, p + 4 * 2 * BR);
     } else {
-      return *reinterpret_cast<const u32x4*>(stage + first + at[j] + 32 * 128 * i);
+      return *reinterpret_cast<const u32x4*>(stage + first + at[j] + 32 * 2 * SK * i);
     }
   }
 };
 
 // x: T rows, w: N rows, sums of K; w is K-major, x is if XT.  The sums of split blockIdx / tiles, of `per` steps each, go to
 // out + split * T * N (fp32 parts, where there are several).
-template <bool XT, int BM, int BN, int WM, int WN, int S, int kSpread>
+template <bool XT, int BM, int BN, int WM, int WN, int SK, int S, int kSpread>
 __global__ __launch_bounds__(64 * WM * WN, 2) void grad_tile_kernel(LinearArgs a, int m_tiles, int n_tiles, int per) {
   a.act = kActNone;  // known to the compiler
   constexpr int NW = WM * WN;
   constexpr int AT = BM / WM / 32, BT = BN / WN / 32;  // token and weight MFMA tiles of a wave
-  typedef Source<XT, BM, NW> SX;
-  typedef Source<true, BN, NW> SW;
-  constexpr int UA = SX::kLoads, UB = SW::kLoads, LD = UA + UB, kStage = (BM + BN) * 128;
+  typedef Source<XT, BM, NW, SK> SX;
+  typedef Source<true, BN, NW, SK> SW;
+  constexpr int UA = SX::kLoads, UB = SW::kLoads, LD = UA + UB;
+  constexpr int kXStage = BM * 2 * SK, kStage = kXStage + BN * 2 * SK, kSub = SK / 16;
   static_assert((S == 2 || S == 4) && kSpread <= kSub && LD % kSpread == 0, "ring");
   // one object per stage: the compiler tracks direct loads per object
   __shared__ __align__(16) uint8_t st0[kStage], st1[kStage], st2[S == 4 ? kStage : 16], st3[S == 4 ? kStage : 16];
@@ -135,26 +135,26 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void grad_tile_kernel(LinearArgs a
   const int band_rows = min(kBand, m_tiles - band * kBand);
   const int64_t t0 = (int64_t)(band * kBand + in_band % band_rows) * BM;
   const int n0 = in_band / band_rows * BN;  // first output column
-  const int64_t k_first = (int64_t)split * per * kStepK, k_end = min((int64_t)a.K, k_first + (int64_t)per * kStepK);
-  const int nk = (int)((k_end - k_first + kStepK - 1) / kStepK);
+  const int64_t k_first = (int64_t)split * per * SK, k_end = min((int64_t)a.K, k_first + (int64_t)per * SK);
+  const int nk = (int)((k_end - k_first + SK - 1) / SK);
 
   SX sx;
   SW sw;
   sx.init(a.x, t0, a.T, a.K, w, lane);
   sw.init(a.w, n0, a.N, a.K, w, lane);
-  Reader<XT, BM, AT> rx;
-  Reader<true, BN, BT> rw;
+  Reader<XT, BM, AT, SK> rx;
+  Reader<true, BN, BT, SK> rw;
   rx.init(AT * wm, lane);
   rw.init(BT * wn, lane);
   // the stage buffers by index (a constant wherever they are used)
   auto stage = [&](int d) -> uint8_t* { return d == 0 ? st0 : d == 1 ? st1 : d == 2 ? st2 : st3; };
   // direct load i of stage kb into buffer d: the token operand's, then the weights'
   auto load_one = [&](int d, int kb, int i) {
-    const int64_t k0 = k_first + (int64_t)kb * kStepK;
+    const int64_t k0 = k_first + (int64_t)kb * SK;
     if (i < UA)
       sx.load(stage(d), i, k0, k_end, a.T, t0, w);
     else
-      sw.load(stage(d) + BM * 128, i - UA, k0, k_end, a.N, n0, w);
+      sw.load(stage(d) + kXStage, i - UA, k0, k_end, a.N, n0, w);
   };
   struct Ops {
     u32x4 x[AT], w[BT];
@@ -166,7 +166,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void grad_tile_kernel(LinearArgs a
     for (int b = 0; b < BT; ++b)
 #pragma unroll
       for (int i = 0; i < 16; ++i) acc[t][b][i] = 0.f;
-  auto read_w = [&](Ops& o, int d, int j, int b) { o.w[b] = rw.read(stage(d) + BM * 128, j, b); };
+  auto read_w = [&](Ops& o, int d, int j, int b) { o.w[b] = rw.read(stage(d) + kXStage, j, b); };
   auto read_x = [&](Ops& o, int d, int j, int t) { o.x[t] = rx.read(stage(d), j, t); };
 
 #pragma unroll
@@ -319,22 +319,27 @@ __global__ __launch_bounds__(256) void join_kernel(const float* parts, int split
 }
 
 // Which tiles, and over how many splits of the sum: what takes the least time by this model.  A round is the workgroups that
-// run at once; it takes base + slope per 1024 of the sum's length (us, measured on sums of 1024, 2048 and 4096 over full
-// rounds):
-//   rows x columns                           at once    base   slope
-//   64 x 64, four stages                     256        6      2.8
-//   64 x 64, four stages                     512        5.5    6
-//   128 x 128, eight waves, four stages      256        7      7.8
-//   256 x 128, eight waves, two stages       256        8      14.5
-//   256 x 256, eight waves, two stages       256        12.5   23.6
-// (128 x 128 by four waves, two workgroups to a CU: 8 and 15 for 512, never the least.)  The parts of several splits are
-// written and read once more in fp32, at about 5 TB/s and 4 us for the launch.
+// run at once; it takes base + slope per 1024 of the sum's length (us, measured on sums of 1024 to 8192 over full rounds):
+//   rows x columns                                        at once    base   slope
+//   64 x 64, four stages                                  256        6      2.8
+//   64 x 64, four stages                                  512        5.5    6
+//   128 x 128, eight waves, four stages                   256        7      7.8
+//   256 x 128 (128 x 256 where x is not K-major),
+//   eight waves, four stages of 32 k                      256        8      13.6
+//   256 x 256, eight waves, two stages                    256        12.5   23.7
+// The parts of several splits are written and read once more in fp32, at about 5 TB/s and 4 us for the launch.
+// Not kept (us at 8192 x 4096, sums of 4096, and 4096 x 2048, sums of 8192, the kept ones 216 and 118): 256 x 128 in two
+// stages of 64 k 273 and 149; 256 x 256 in four stages of 32 k 219 and 173, by four waves with the sums in the
+// accumulation registers 220 and 174; 128 x 128 by four waves, two workgroups to a CU, 257 and 135.  Without the direct
+// loads 256 x 256 takes 178, without the operand reads 184: both pass through LDS, and their 256 KB a step take longer
+// there (1024 cycles for the loads' writes at 64 bytes a cycle, 1536 for the reads at 128) than the step's MFMAs (2048).
+constexpr int kStepK = 64;  // splits are counted in
 enum Variant { kTile64, kTile128, kTile256x128, kTile256 };
 struct Plan {
   Variant tiles;
   int splits, per;  // steps of a split
 };
-Plan choose(int64_t T, int64_t N, int64_t K) {
+Plan choose(int64_t T, int64_t N, int64_t K, bool x_k_major) {
   Plan best{kTile64, 1, 0};
   double least = 1e30;
   const int64_t steps = (K + kStepK - 1) / kStepK;
@@ -351,36 +356,42 @@ Plan choose(int64_t T, int64_t N, int64_t K) {
   consider(kTile64, 64, 64, 256, 6.0, 2.8);
   consider(kTile64, 64, 64, 512, 5.5, 6.0);
   consider(kTile128, 128, 128, 256, 7.0, 7.8);
-  consider(kTile256x128, 256, 128, 256, 8.0, 14.5);
-  consider(kTile256, 256, 256, 256, 12.5, 23.6);
+  consider(kTile256x128, x_k_major ? 256 : 128, x_k_major ? 128 : 256, 256, 8.0, 13.6);
+  consider(kTile256, 256, 256, 256, 12.5, 23.7);
   return best;
 }
 
-template <bool XT, int BM, int BN, int WM, int WN, int S, int kSpread>
+template <bool XT, int BM, int BN, int WM, int WN, int SK, int S, int kSpread>
 hipError_t go(const LinearArgs& a, const Plan& p, hipStream_t s) {
   const int m_tiles = (a.T + BM - 1) / BM, n_tiles = (a.N + BN - 1) / BN;
-  grad_tile_kernel<XT, BM, BN, WM, WN, S, kSpread>
-      <<<(unsigned)((int64_t)m_tiles * n_tiles * p.splits), 64 * WM * WN, 0, s>>>(a, m_tiles, n_tiles, p.per);
+  grad_tile_kernel<XT, BM, BN, WM, WN, SK, S, kSpread>
+      <<<(unsigned)((int64_t)m_tiles * n_tiles * p.splits), 64 * WM * WN, 0, s>>>(a, m_tiles, n_tiles, p.per * (kStepK / SK));
   return hipGetLastError();
 }
 
 template <bool XT>
 hipError_t launch(const LinearArgs& a, const Plan& p, hipStream_t s) {
-  if (p.tiles == kTile64) return go<XT, 64, 64, 2, 2, 4, 1>(a, p, s);
-  if (p.tiles == kTile128) return go<XT, 128, 128, 4, 2, 4, 2>(a, p, s);
-  if (p.tiles == kTile256x128) return go<XT, 256, 128, 4, 2, 2, 1>(a, p, s);
-  return go<XT, 256, 256, 2, 4, 2, 2>(a, p, s);
+  if (p.tiles == kTile64) return go<XT, 64, 64, 2, 2, 64, 4, 1>(a, p, s);
+  if (p.tiles == kTile128) return go<XT, 128, 128, 4, 2, 64, 4, 2>(a, p, s);
+  if (p.tiles == kTile256x128) {
+    // the K-major operand is the wide one: rows of 32 k of the other are half a cache line
+    if constexpr (XT)
+      return go<XT, 256, 128, 4, 2, 32, 4, 1>(a, p, s);
+    else
+      return go<XT, 128, 256, 2, 4, 32, 4, 1>(a, p, s);
+  }
+  return go<XT, 256, 256, 2, 4, 64, 2, 2>(a, p, s);
 }
 
 }  // namespace
 
-size_t grad_product_ws_bytes(int64_t T, int64_t N, int64_t K) {
-  const Plan p = choose(T, N, K);
+size_t grad_product_ws_bytes(int64_t T, int64_t N, int64_t K, bool x_k_major) {
+  const Plan p = choose(T, N, K, x_k_major);
   return p.splits > 1 ? (size_t)p.splits * T * N * 4 : 0;
 }
 
 hipError_t launch_grad_product(const LinearArgs& a, bool x_k_major, float* parts, hipStream_t s) {
-  const Plan p = choose(a.T, a.N, a.K);
+  const Plan p = choose(a.T, a.N, a.K, x_k_major);
   if (p.splits == 1) return x_k_major ? launch<true>(a, p, s) : launch<false>(a, p, s);
   LinearArgs part = a;
   part.out = parts;
