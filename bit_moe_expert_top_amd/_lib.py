@@ -619,7 +619,8 @@ def moe_route_scored(logits: torch.Tensor, k: int, score: str = "softmax", bias=
 class MoeBlock:
     """A MoE block around one layer's routed experts: norm weight, router (weight [E][H], or fewer rows where
     the last experts are not routed to, bias for balance and the arguments of moe_route_scored) and an optional
-    shared expert, bf16 (ws1 [2Is][H], ws2 [H][Is]) or MXFP8 (ws1 and ws2 as pairs (elements, scales)).  All on
+    shared expert, bf16 (ws1 [2Is][H], ws2 [H][Is]), MXFP8 (ws1 and ws2 as pairs (elements, e8m0 scales)) or FP8 with a
+    scale per block of 128 (pairs (elements, fp32 scales), ws1 as moe_linear_fp8 takes it for swiglu).  All on
     the experts' device; what does not fit them is refused here, and by the next block_forward after an
     attribute is set."""
 
@@ -649,6 +650,14 @@ def _route_status(E: int, k: int, score: str = "softmax", n_group: int = 1, topk
                                 1 if renormalize else 0, scale, None, None, None)
 
 
+def _shared_kind(m) -> str:
+    """The type of a shared expert's matrix: a pair's scales are e8m0 bytes (MXFP8) or fp32 (a block of 128 each)."""
+    if not isinstance(m, (tuple, list)):
+        return "bf16"
+    _require(len(m) == 2, "ws1 and ws2", "pairs (elements, scales)")
+    return "fp8" if m[1].dtype == torch.float32 else "mxfp8"
+
+
 def _check_block(blk: MoeBlock):
     """Refuses operands that do not fit the layer: block_forward would send ids to experts that are not
     there or read past the rows, or fail with the residual stream already updated."""
@@ -667,31 +676,33 @@ def _check_block(blk: MoeBlock):
         raise ValueError(f"route: expected arguments of moe_route_scored, got {blk.route}") from error
     _require(status == 0, "route", f"arguments that moe_route_scored takes for {E} experts, got {blk.route}")
 
-    def matrix(name, m, rows, cols, mx):
-        if mx:
+    def matrix(name, m, rows, cols, kind, parts=1):
+        if kind == "mxfp8":
             _arg(m[1], _E8M0, (rows, cols // 32), dev, f"{name} scales")
-        m = m[0] if mx else m
-        _require(_arg(m, _E4M3 if mx else _BF16, (rows, cols), dev, name) is not None, name, "a matrix")
-        _require(m.data_ptr() % 16 == 0 and cols % (32 if mx else 8) == 0, name,
-                 "16-byte aligned rows of whole MXFP8 blocks" if mx else "16-byte aligned rows")
+        elif kind == "fp8":
+            _arg(m[1], (torch.float32,), (parts * ((rows // parts + 127) // 128), (cols + 127) // 128), dev, f"{name} scales")
+        m = m if kind == "bf16" else m[0]
+        _require(_arg(m, _BF16 if kind == "bf16" else _E4M3, (rows, cols), dev, name) is not None, name, "a matrix")
+        whole = {"bf16": 8, "mxfp8": 32, "fp8": 16}[kind]
+        _require(m.data_ptr() % 16 == 0 and cols % whole == 0, name, f"16-byte aligned rows of a multiple of {whole} values")
 
-    matrix("router_weight", blk.router_weight, E, H, False)
+    matrix("router_weight", blk.router_weight, E, H, "bf16")
     _require((blk.ws1 is None) == (blk.ws2 is None), "ws1 and ws2", "both or none, they go together")
     if blk.ws1 is not None:
-        mx = isinstance(blk.ws1, (tuple, list))
-        _require(isinstance(blk.ws2, (tuple, list)) == mx, "ws2", "the type of ws1 (bf16, or MXFP8 pairs)")
-        rows = (blk.ws1[0] if mx else blk.ws1).shape[0]
+        kind = _shared_kind(blk.ws1)
+        _require(_shared_kind(blk.ws2) == kind, "ws2", "the type of ws1 (bf16, MXFP8 or block-scaled FP8 pairs)")
+        rows = (blk.ws1 if kind == "bf16" else blk.ws1[0]).shape[0]
         _require(rows % 2 == 0 and rows > 0, "ws1", "gate and up rows, [2Is][H]")
-        matrix("ws1", blk.ws1, rows, H, mx)
-        matrix("ws2", blk.ws2, H, rows // 2, mx)
+        matrix("ws1", blk.ws1, rows, H, kind, parts=2)
+        matrix("ws2", blk.ws2, H, rows // 2, kind)
     object.__setattr__(blk, "checked", True)
 
 
 def block_forward(blk: MoeBlock, x: torch.Tensor, residual: torch.Tensor | None):
     """One MoE block of a pre-norm residual stream: x (the previous sublayer's output, fp32 or bf16) joins
     the residual stream in place (None: x is the stream), its norm is routed and run through the experts and the
-    shared expert.  Returns every intermediate; ``out`` is the block's output (fp32, or bf16 with an MXFP8 shared
-    expert), to be added to ``residual`` by the next norm."""
+    shared expert.  Returns every intermediate; ``out`` is the block's output (fp32, or bf16 with an MXFP8 or FP8
+    shared expert), to be added to ``residual`` by the next norm."""
     if not blk.checked:
         _check_block(blk)
     w, dev = blk.experts, next(iter(blk.experts.t.values())).device
@@ -701,7 +712,8 @@ def block_forward(blk: MoeBlock, x: torch.Tensor, residual: torch.Tensor | None)
     _require(2 * T * H < 1 << 32 and T * blk.k < 1 << 31, "x", "fewer tokens, the experts take 2 T H < 2^32")
     for name, t in (("x", x), ("residual", residual)):
         _require((_arg(t, tuple(_FLOAT_DT), (T, H), dev, name) or 0) % 16 == 0, name, "16-byte alignment")
-    mx = isinstance(blk.ws1, (tuple, list))
+    kind = _shared_kind(blk.ws1)
+    mx = kind == "mxfp8"
     with torch.cuda.device(dev):
         y = torch.empty((T, H), dtype=torch.int16, device=dev)
         q = torch.empty((T, H), dtype=torch.uint8, device=dev) if mx else None
@@ -717,6 +729,11 @@ def block_forward(blk: MoeBlock, x: torch.Tensor, residual: torch.Tensor | None)
             h = moe_linear(q, blk.ws1[0], x_scales=qs, w_scales=blk.ws1[1], act="swiglu")
             hq, hs = moe_mxfp8_quantize(h)
             out = moe_linear(hq, blk.ws2[0], x_scales=hs, w_scales=blk.ws2[1], residual=routed)
+        elif kind == "fp8":
+            q, qs = moe_fp8_quantize(y)
+            h = moe_linear_fp8(q, qs, *blk.ws1, act="swiglu")
+            hq, hs = moe_fp8_quantize(h)
+            out = moe_linear_fp8(hq, hs, *blk.ws2, residual=routed)
         elif blk.ws1 is not None:
             h = moe_linear(y, blk.ws1, act="swiglu")
             out = moe_linear(h, blk.ws2, residual=routed, out_dtype=torch.float32)

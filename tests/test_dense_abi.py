@@ -157,3 +157,42 @@ def z(*shape, dtype=BF):
 def test_binding_refusals(L, call):
     with pytest.raises(ValueError):
         call(L)
+
+
+# ------------------------------------------------------------------ the block's shared expert in FP8
+@pytest.fixture(scope="module")
+def layer(L):
+    from _helpers import FMT, layer_arrays
+
+    sp, arrays = layer_arrays("tiny")
+    return sp, L.DeviceWeights(FMT[sp["fmt"]], sp["E"], sp["H"], sp["I"], arrays, device="cpu")
+
+
+def fp8_pair(rows, cols, parts=1):
+    return (torch.zeros(rows, cols, dtype=torch.uint8),
+            torch.zeros(parts * ((rows // parts + 127) // 128), (cols + 127) // 128))
+
+
+def fp8_block(L, layer, ws1, ws2):
+    sp, dw = layer
+    return L.MoeBlock(dw, sp["k"], z(sp["H"]), z(sp["E"], sp["H"]), ws1=ws1, ws2=ws2)
+
+
+@pytest.mark.parametrize("Is", [16, 128, 144, 256])
+def test_block_takes_block_scaled_shared_experts(L, layer, Is):
+    H = layer[0]["H"]
+    fp8_block(L, layer, fp8_pair(2 * Is, H, 2), list(fp8_pair(H, Is)))
+
+
+@pytest.mark.parametrize("ws1,ws2,match", [
+    (lambda H: fp8_pair(288, H), lambda H: fp8_pair(H, 144), "ws1"),                 # gate and up have block rows of their own
+    (lambda H: fp8_pair(288, H, 2), lambda H: fp8_pair(H, 160), "ws2"),
+    (lambda H: fp8_pair(16, H, 2), lambda H: fp8_pair(H, 8), "ws2"),                 # rows of 8 values
+    (lambda H: fp8_pair(288, H, 2), lambda H: z(H, 144), "ws2"),                     # FP8 and bf16 mixed
+    (lambda H: fp8_pair(256, H, 2), lambda H: (fp8_pair(H, 128)[0], torch.zeros(H, 4, dtype=torch.uint8)), "ws2"),  # and MXFP8
+    (lambda H: fp8_pair(288, H, 2) + (None,), lambda H: fp8_pair(H, 144), "pairs"),
+])
+def test_block_refuses_other_shared_experts(L, layer, ws1, ws2, match):
+    H = layer[0]["H"]
+    with pytest.raises(ValueError, match=match):
+        fp8_block(L, layer, ws1(H), ws2(H))

@@ -12,7 +12,7 @@ import torch
 from oracle import block as OB
 from oracle import dense as OD
 
-from _helpers import KAPPA, host
+from _helpers import KAPPA, device_layer, host
 
 pytestmark = pytest.mark.gpu
 
@@ -580,3 +580,59 @@ def test_same_bits_on_every_call(L):
             run()
             for k in b:
                 assert torch.equal(b[k], first[k]), (T, k)
+
+
+# ------------------------------------------------------------------ the block with a block-scaled FP8 shared expert
+def block_fp8(L, Is=144):
+    sp, dw = device_layer("tiny")
+    H, E = sp["H"], sp["E"]
+    r = np.random.default_rng(43)
+    w1, w2 = fp8_operand(L, bf16(r, 2 * Is, H, scale=H**-0.5), 128, True), fp8_operand(L, bf16(r, H, Is, scale=Is**-0.5), 128)
+    wn, wr = cuda(1 + 0.1 * r.normal(size=H), torch.bfloat16), bf16(r, E, H, scale=1 / 16)
+    blk = L.MoeBlock(dw, sp["k"], wn, wr, route=dict(score="sigmoid"), ws1=w1[:2], ws2=w2[:2])
+    return H, blk, L.MoeBlock(dw, sp["k"], wn, wr, route=dict(score="sigmoid")), w1[2], w2[2]
+
+
+@pytest.mark.parametrize("T", [0, 1, 16, 130])
+@pytest.mark.parametrize("Is", [144, 256])
+def test_block(L, T, Is):
+    """The shared expert's part on the block's own norm and routed sum; the rest as without one."""
+    H, blk, bare, v1, v2 = block_fp8(L, Is)
+    r = np.random.default_rng(T)
+    x, res = cuda(r.normal(size=(T, H))), bf16(r, T, H)
+    res2 = res.clone()
+    o, plain = L.block_forward(blk, x, res), L.block_forward(bare, x, res2)
+    torch.cuda.synchronize()
+    for k in ("y", "logits", "ids", "gates", "perm", "routed"):
+        assert torch.equal(o[k], plain[k]), k
+    assert torch.equal(res, res2) and o["out"].shape == (T, H)
+    if T == 0:
+        return
+    q, s = OD.fp8_quantize(values(o["y"]), 1)
+    np.testing.assert_array_equal(host(o["q_scales"]), s)
+    h = OB.linear(OD.fp8_values(q, s, 1), v1, act_name="swiglu")
+    hv = values(o["h"])
+    # a rounding to bf16, and the FP8 cores' sums through the gate (their KAPPA on both halves)
+    assert np.linalg.norm(hv - h) <= (2.0**-8 + 3 * KAPPA) * np.linalg.norm(h)
+    out = OB.linear(OD.fp8_values(*OD.fp8_quantize(hv, 1), 1), v2, residual=values(o["routed"]))
+    assert np.linalg.norm(values(o["out"]) - out) <= (2.0**-8 + KAPPA) * np.linalg.norm(out)
+
+
+def test_block_captured(L):
+    H, blk, _, _, _ = block_fp8(L)
+    x, res = torch.randn(40, H, device="cuda"), torch.randn(40, H, device="cuda").bfloat16()
+    L.block_forward(blk, x.clone(), res.clone())
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        captured = L.block_forward(blk, x, res)
+    for i in range(4):
+        x.copy_(torch.randn(40, H, device="cuda"))
+        res.copy_(torch.randn(40, H, device="cuda").bfloat16())
+        eager = res.clone()
+        graph.replay()
+        torch.cuda.synchronize()
+        got = captured["out"].clone()
+        want = L.block_forward(blk, x, eager)
+        torch.cuda.synchronize()
+        assert torch.equal(got, want["out"]) and torch.equal(res, eager)
