@@ -67,7 +67,7 @@ hipError_t launch_linear(const LinearArgs& a, LinearKind kind, hipStream_t s);
 hipError_t launch_fp8_quantize(const void* x, bool x_f32, int64_t rows, int K, int by, uint8_t* q, float* scales,
                                hipStream_t s);
 
-// ---- gradients (grad.hip)
+// ---- gradients (grad.hip; glu_grad.hip for the gate)
 struct GradArgs {
   const uint16_t* dy;  // bf16 [T][N]
   const uint16_t* x;   // bf16 [T][K]
@@ -78,10 +78,6 @@ struct GradArgs {
   int accumulate;      // dw is added to
   int T, N, K;
 };
-// The products behind them (grad_tile.hip): out [T][N] = x W^T with w K-major ([K][N]) and x K-major or not; of a, what
-// moe_linear's epilogue needs for act none; a residual is out itself.  parts: grad_product_ws_bytes bytes.
-size_t grad_product_ws_bytes(int64_t T, int64_t N, int64_t K, bool x_k_major);
-hipError_t launch_grad_product(const LinearArgs& a, bool x_k_major, float* parts, hipStream_t s);
 size_t grad_ws_bytes(int64_t T, int64_t N, int64_t K);
 hipError_t launch_grad(const GradArgs& a, uint8_t* ws, hipStream_t s);
 // da [T][2 I] from dh [T][I] and the pre-activations a [T][2 I]
