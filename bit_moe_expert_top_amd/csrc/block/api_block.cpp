@@ -174,6 +174,9 @@ moe_status moe_fp8_quantize(const void* x, int32_t x_dtype, int64_t rows, int32_
   if (K % 16 || K > kMaxLinear || rows > kMaxLinearRows) return MOE_ERR_UNSUPPORTED;
   if (rows == 0) return MOE_OK;
   if (!x || !q || !scales || !aligned(x, 16) || !aligned(q, 8) || !aligned(scales, 4)) return MOE_ERR_INVALID_ARG;
+  const Span sx{x, (size_t)rows * K * (x_dtype == MOE_DT_F32 ? 4 : 2)}, sq{q, (size_t)rows * K};
+  const Span ss{scales, (size_t)((rows + block_rows - 1) / block_rows) * ((K + 127) / 128) * 4};
+  if (shares(sq, sx, ss) || shares(ss, sx)) return MOE_ERR_INVALID_ARG;
   return from_hip(launch_fp8_quantize(x, x_dtype == MOE_DT_F32, rows, K, block_rows, q, scales, as_stream(stream)));
 }
 
@@ -193,6 +196,10 @@ moe_status moe_linear_fp8(const uint8_t* x, const float* x_scales, const uint8_t
     return MOE_ERR_INVALID_ARG;
   const size_t outs = (size_t)T * (gated ? N / 2 : N);
   if (residual && (residual != out || residual_dtype != MOE_DT_BF16) && overlap(residual, outs * rb, out, outs * 2))
+    return MOE_ERR_INVALID_ARG;
+  const size_t kb = ((size_t)K + 127) / 128, blocks = gated ? 2 * (((size_t)N / 2 + 127) / 128) : ((size_t)N + 127) / 128;
+  if (shares(Span{out, outs * 2}, Span{x, (size_t)T * K}, Span{w, (size_t)N * K}, Span{x_scales, T * kb * 4},
+             Span{w_scales, blocks * kb * 4}, Span{bias, (size_t)N * 4}))
     return MOE_ERR_INVALID_ARG;
   LinearArgs a{};
   a.x = x;
@@ -248,10 +255,10 @@ moe_status moe_linear_backward(const uint16_t* dy, const uint16_t* x, const uint
   const Span sdy{dy, (size_t)T * N * 2}, sws{ws, ws_bytes};
   const moe_status bad = grad_args(g, dy, x, w, T, N, K, dx, dx_dtype, dw, dw_dtype, accumulate, sdy, sws);
   if (bad != MOE_OK) return bad;
-  const size_t need = grad_ws_bytes(T, N, K);
-  if (ws_bytes < need) return MOE_ERR_WORKSPACE;
-  if (need && (!ws || !aligned(ws, 16))) return MOE_ERR_INVALID_ARG;
-  return from_hip(launch_grad(g, static_cast<uint8_t*>(ws), as_stream(stream)));
+  const GradPlan plan = plan_grad(g);
+  if (ws_bytes < plan.ws_bytes) return MOE_ERR_WORKSPACE;
+  if (plan.ws_bytes && (!ws || !aligned(ws, 16))) return MOE_ERR_INVALID_ARG;
+  return from_hip(launch_grad(g, plan, ws, as_stream(stream)));
 }
 
 size_t moe_glu_backward_ws_bytes(int32_t T, int32_t I, int32_t K) {
@@ -270,14 +277,15 @@ moe_status moe_glu_backward(const uint16_t* dh, const uint16_t* a, const uint16_
   const moe_status bad = grad_args(g, da, x, w, T, 2 * I, K, dx, dx_dtype, dw, dw_dtype, accumulate, sdh, sa, sws);
   if (bad != MOE_OK) return bad;
   if (T > 0 && shares(sws, sdh, sa)) return MOE_ERR_INVALID_ARG;
-  const size_t need = da_bytes(T, I) + grad_ws_bytes(T, 2 * I, K);
+  const GradPlan plan = plan_grad(g);
+  const size_t need = da_bytes(T, I) + plan.ws_bytes;
   if (ws_bytes < need) return MOE_ERR_WORKSPACE;
   if (need && (!ws || !aligned(ws, 16))) return MOE_ERR_INVALID_ARG;
   if (T > 0) {
     const hipError_t e = launch_glu_grad(dh, a, T, I, act, da, as_stream(stream));
     if (e != hipSuccess) return from_hip(e);
   }
-  return from_hip(launch_grad(g, static_cast<uint8_t*>(ws) + da_bytes(T, I), as_stream(stream)));
+  return from_hip(launch_grad(g, plan, static_cast<uint8_t*>(ws) + da_bytes(T, I), as_stream(stream)));
 }
 
 }  // extern "C"

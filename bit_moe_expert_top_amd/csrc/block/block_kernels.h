@@ -78,8 +78,23 @@ struct GradArgs {
   int accumulate;      // dw is added to
   int T, N, K;
 };
-size_t grad_ws_bytes(int64_t T, int64_t N, int64_t K);
-hipError_t launch_grad(const GradArgs& a, uint8_t* ws, hipStream_t s);
+// How a call is laid out: its tiles, and the splits of each sum (of per steps) that ws_bytes hold the parts of.
+enum GradVariant { kTile64, kTile128, kTile256x128, kTile256 };
+struct GradSplit {
+  int splits, per, m_tiles, n_tiles;
+};
+struct GradTiles {
+  GradVariant tiles;
+  GradSplit dx, dw;
+  bool dw_first;
+};
+struct GradPlan {
+  GradTiles plan;
+  size_t ws_bytes;
+};
+GradPlan plan_grad(const GradArgs& a);
+size_t grad_ws_bytes(int64_t T, int64_t N, int64_t K);  // of any call of these sizes: dx, dw or both
+hipError_t launch_grad(const GradArgs& a, const GradPlan& plan, void* ws, hipStream_t s);
 // da [T][2 I] from dh [T][I] and the pre-activations a [T][2 I]
 hipError_t launch_glu_grad(const uint16_t* dh, const uint16_t* a, int T, int I, int act, uint16_t* da, hipStream_t s);
 

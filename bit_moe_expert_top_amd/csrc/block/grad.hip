@@ -13,6 +13,7 @@
 // A step loads and waits without a branch: past the last k it loads zeros.  The rest is moe_linear's: the weight tile is the
 // MFMA's A operand, operands are read one sub-step of 16 k ahead, the sums pass through LDS in the epilogue.
 #include <algorithm>
+#include <cmath>
 #include <type_traits>
 
 #include "linear_dev.h"
@@ -367,28 +368,20 @@ __global__ __launch_bounds__(256) void join_kernel(Join dx, Join dw) {
 // accumulation registers 220 and 174; 128 x 128 by four waves, two workgroups to a CU, 257 and 135.  Without the direct
 // loads 256 x 256 takes 178, without the operand reads 184: both pass through LDS, and their 256 KB a step take longer
 // there (1024 cycles for the loads' writes at 64 bytes a cycle, 1536 for the reads at 128) than the step's MFMAs (2048).
-enum Variant { kTile64, kTile128, kTile256x128, kTile256 };
+using Variant = GradVariant;
+using Plan = GradTiles;
+using Split = GradSplit;
 struct Sum {  // of one product: rows, columns, length; rows = 0 where it is not wanted
   int64_t T, N, K;
 };
-struct Split {
-  int splits, per, m_tiles, n_tiles;
-};
-struct Plan {
-  Variant tiles;
-  Split dx, dw;
-  bool dw_first;
-};
 
 // The time until n1 workgroups of t1 each and then n2 of t2 are done, on `at_once` places.
-double makespan(int64_t n1, double t1, int64_t n2, double t2, int at_once) {
-  const int64_t rest = n1 % at_once, full = n1 / at_once;
-  double a = (double)(full + 1) * t1, b = (double)full * t1;  // rest places are free at a, the others at b
-  if (rest == 0) a = b;
-  const double end = rest ? a : b;
-  if (n2 == 0) return end;
-  int64_t left = n2;
-  while (left > 0) {
+double makespan(double n1, double t1, double n2, double t2, double at_once) {
+  const double full = std::floor(n1 / at_once), rest = n1 - full * at_once;
+  double a = (full + (rest > 0 ? 1 : 0)) * t1, b = full * t1;  // rest places are free at a, the others at b
+  const double end = a, whole = std::max(std::floor(n2 / at_once) - 1, 0.0);
+  a += whole * t2, b += whole * t2;
+  for (double left = n2 - whole * at_once; left > 0;) {
     if (b <= a) {
       left -= at_once - rest;
       b += t2;
@@ -397,44 +390,59 @@ double makespan(int64_t n1, double t1, int64_t n2, double t2, int at_once) {
       a += t2;
     }
   }
-  return std::max(std::max(a, b), end);
+  return n2 > 0 ? std::max(std::max(a, b), end) : end;
 }
 
+// A call takes about half a microsecond: what does not depend on the tiles is taken out of their loops.
 Plan choose(const Sum& dx, const Sum& dw) {
+  constexpr int kSplits = 5;  // 1, 2, 4, 8, 16
+  struct Option {
+    int splits, per;
+    double join;
+  };
+  auto options = [](const Sum& p, Option(&o)[kSplits]) {
+    if (p.T == 0) {
+      o[0] = {1, 0, 0.0};
+      return 1;
+    }
+    const int steps = std::max((int)((p.K + kStepK - 1) / kStepK), 1);
+    int n = 0;
+    for (int i = 0; i < kSplits; ++i) {
+      const int per = (steps + (1 << i) - 1) >> i, splits = (steps + per - 1) / per;
+      if (i > 0 && (per < 4 || splits == o[n - 1].splits)) break;
+      o[n++] = {splits, per, splits > 1 ? 1.6e-6 * (double)p.T * (double)p.N * splits : 0.0};
+    }
+    return n;
+  };
+  Option ox[kSplits], ow[kSplits];
+  const int cx = options(dx, ox), cw = options(dw, ow);
   Plan best{};
   double least = 1e30;
-  auto split = [](const Sum& p, int bm, int bn, int s) {
-    Split r{1, 0, 0, 0};
-    if (p.T == 0) return r;
-    const int64_t steps = std::max<int64_t>((p.K + kStepK - 1) / kStepK, 1), per = (steps + s - 1) / s;
-    if (s > 1 && per < 4) return Split{0, 0, 0, 0};
-    return Split{(int)((steps + per - 1) / per), (int)per, (int)((p.T + bm - 1) / bm), (int)((p.N + bn - 1) / bn)};
-  };
-  auto consider = [&](Variant v, int bx, int by, int at_once, double base, double slope) {
-    for (int i = 1; i <= 16; i *= 2) {
-      const Split x = split(dx, bx, by, i);
-      const int64_t nx = (int64_t)x.m_tiles * x.n_tiles * x.splits;
-      if (x.splits == 0 || (i > 1 && (x.splits < i / 2 + 1 || nx > 512))) break;
-      const double tx = base + slope * x.per / 16;
-      for (int j = 1; j <= 16; j *= 2) {
-        const Split w = split(dw, by, bx, j);
-        const int64_t nw = (int64_t)w.m_tiles * w.n_tiles * w.splits;
-        if (w.splits == 0 || (j > 1 && (w.splits < j / 2 + 1 || nw > 512))) break;
-        const double tw = base + slope * w.per / 16;
+  // tiles of dx of 2^bx rows and 2^by columns, of dW turned round
+  auto consider = [&](Variant v, int bx, int by, double at_once, double base, double slope) {
+    auto tiles = [](int64_t n, int b) { return (int)((n + ((int64_t)1 << b) - 1) >> b); };
+    const int xm = tiles(dx.T, bx), xn = tiles(dx.N, by), wm = tiles(dw.T, by), wn = tiles(dw.N, bx);
+    for (int i = 0; i < cx; ++i) {
+      const double nx = (double)xm * xn * ox[i].splits, tx = base + slope * ox[i].per / 16;
+      if (i > 0 && nx > 512) break;
+      for (int j = 0; j < cw; ++j) {
+        const double nw = (double)wm * wn * ow[j].splits, tw = base + slope * ow[j].per / 16;
+        if (j > 0 && nw > 512) break;
+        const double join = ox[i].join + ow[j].join + (ox[i].splits + ow[j].splits > 2 ? 4.0 : 0.0);
+        if ((nx * tx + nw * tw) / at_once + join >= least) continue;
         const bool dw_first = tw > tx;
-        double t = dw_first ? makespan(nw, tw, nx, tx, at_once) : makespan(nx, tx, nw, tw, at_once);
-        if (x.splits > 1 || w.splits > 1) t += 4;
-        if (x.splits > 1) t += 1.6e-6 * dx.T * dx.N * x.splits;
-        if (w.splits > 1) t += 1.6e-6 * dw.T * dw.N * w.splits;
-        if (t < least) least = t, best = {v, x, w, dw_first};
+        const double t = join + (dw_first ? makespan(nw, tw, nx, tx, at_once) : makespan(nx, tx, nw, tw, at_once));
+        if (t >= least) continue;
+        least = t;
+        best = {v, {ox[i].splits, ox[i].per, xm, xn}, {ow[j].splits, ow[j].per, wm, wn}, dw_first};
       }
     }
   };
-  consider(kTile64, 64, 64, 256, 6.0, 2.8);
-  consider(kTile64, 64, 64, 512, 5.5, 6.0);
-  consider(kTile128, 128, 128, 256, 7.0, 7.8);
-  consider(kTile256x128, 128, 256, 256, 8.0, 13.6);
-  consider(kTile256, 256, 256, 256, 12.5, 23.7);
+  consider(kTile128, 7, 7, 256, 7.0, 7.8);
+  consider(kTile64, 6, 6, 256, 6.0, 2.8);
+  consider(kTile64, 6, 6, 512, 5.5, 6.0);
+  consider(kTile256x128, 7, 8, 256, 8.0, 13.6);
+  consider(kTile256, 8, 8, 256, 12.5, 23.7);
   return best;
 }
 
@@ -483,11 +491,17 @@ size_t grad_ws_bytes(int64_t T, int64_t N, int64_t K) {
   return (size_t)most * 4;
 }
 
-hipError_t launch_grad(const GradArgs& g, uint8_t* ws, hipStream_t s) {
+GradPlan plan_grad(const GradArgs& g) {
+  const Sum x = sum_dx(g.dx, g.T, g.N, g.K), w = sum_dw(g.dw, g.T, g.N, g.K);
+  const Plan p = choose(x, w);
+  return {p, (size_t)(parts_of(x, p.dx) + parts_of(w, p.dw)) * 4};
+}
+
+hipError_t launch_grad(const GradArgs& g, const GradPlan& plan, void* ws, hipStream_t s) {
   const Sum x = sum_dx(g.dx, g.T, g.N, g.K), w = sum_dw(g.dw, g.T, g.N, g.K);
   if (x.T == 0 && w.T == 0) return hipSuccess;
-  const Plan p = choose(x, w);
-  float* parts_x = reinterpret_cast<float*>(ws);
+  const Plan& p = plan.plan;
+  float* parts_x = static_cast<float*>(ws);
   float* parts_w = parts_x + parts_of(x, p.dx);
   const Product dx = product(g.dy, g.w, x, p.dx, g.dx, g.dx_f32, false, parts_x);
   const Product dw = product(g.dy, g.x, w, p.dw, g.dw, g.dw_f32, g.accumulate, parts_w);

@@ -126,9 +126,14 @@ __device__ __forceinline__ FourBias load_bias4(const LinearArgs& a, int n) {
 constexpr int kPlain = 0, kSwiglu = 1, kGlu = 2;
 
 // Four bf16 values to p, of which cols lie inside the row.
+template <bool STREAM>
 __device__ __forceinline__ void store_bf16x4(uint16_t* p, const float (&v)[4], bool vec, int cols) {
   if (vec) {
-    *reinterpret_cast<u32x2*>(p) = u32x2{f32x2_to_bf16x2_rne(v[0], v[1]), f32x2_to_bf16x2_rne(v[2], v[3])};
+    const u32x2 q = {f32x2_to_bf16x2_rne(v[0], v[1]), f32x2_to_bf16x2_rne(v[2], v[3])};
+    if (STREAM)
+      __builtin_nontemporal_store(q, reinterpret_cast<u32x2*>(p));
+    else
+      *reinterpret_cast<u32x2*>(p) = q;
     return;
   }
 #pragma unroll
@@ -150,8 +155,8 @@ __device__ __forceinline__ void epilogue4(const LinearArgs& a, int64_t at, int n
   if constexpr (GATED == kGlu) {
     if (a.pre) {
       uint16_t* gate = a.pre + 2 * at - n;  // row t of 2 n_out columns, at = t n_out + n
-      store_bf16x4(gate, v, a.vec, a.n_out - n);
-      store_bf16x4(gate + a.n_out, u, a.vec, a.n_out - n);
+      store_bf16x4<STREAM>(gate, v, a.vec, a.n_out - n);
+      store_bf16x4<STREAM>(gate + a.n_out, u, a.vec, a.n_out - n);
     }
     activate(r, a.glu_act);
 #pragma unroll

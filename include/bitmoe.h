@@ -450,7 +450,8 @@ moe_status moe_route_scored(const float* logits, const float* bias, int32_t T, i
  *   scales   f32 [rows / block_rows rounded up][K / 128 rounded up]; the last blocks may be partial
  * A block of zeros, or of values so small that their scale is 0, has scale 0 and elements 0.  An infinity makes its
  * block's scale infinite (its own element NaN, the others 0), a NaN makes scale and elements NaN.
- * Errors: INVALID_ARG (bad sizes, types or pointers; x not 16-byte, q not 8-byte, scales not 4-byte aligned),
+ * Errors: INVALID_ARG (bad sizes, types or pointers; x not 16-byte, q not 8-byte, scales not 4-byte aligned; arrays that
+ * overlap),
  * UNSUPPORTED (K % 16 != 0; K > 2^20; rows > 2^26). */
 moe_status moe_fp8_quantize(const void* x, int32_t x_dtype, int64_t rows, int32_t K, int32_t block_rows, uint8_t* q,
                             float* scales, void* stream);
@@ -467,7 +468,7 @@ moe_status moe_fp8_quantize(const void* x, int32_t x_dtype, int64_t rows, int32_
  * A block's products are summed by the FP8 matrix cores (not an fp32 sum: see moe_linear), the blocks in fp32.  The order
  * of a row's sums may follow T, so its bits may change with the batch size.
  * Errors: INVALID_ARG (bad sizes, types or pointers; N odd with SwiGLU; x or w not 16-byte aligned; out over part of
- * residual), UNSUPPORTED (K % 16 != 0; N or K > 2^20; T > 2^26). */
+ * residual or over another operand), UNSUPPORTED (K % 16 != 0; N or K > 2^20; T > 2^26). */
 moe_status moe_linear_fp8(const uint8_t* x, const float* x_scales, const uint8_t* w, const float* w_scales, int32_t T,
                           int32_t N, int32_t K, const float* bias, int32_t act, const void* residual,
                           int32_t residual_dtype, uint16_t* out, void* stream);

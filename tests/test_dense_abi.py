@@ -27,6 +27,7 @@ def quantize(L, x=X, dt=2, rows=4, K=64, by=1, q=O, s=XS):
     (dict(rows=-1), -1), (dict(K=0), -1), (dict(dt=3), -1), (dict(dt=0), -1), (dict(by=0), -1), (dict(by=64), -1),
     (dict(K=72), -2), (dict(K=(1 << 20) + 16), -2), (dict(rows=(1 << 26) + 1), -2), (dict(x=None), -1), (dict(q=None), -1),
     (dict(s=None), -1), (dict(x=X + 8), -1), (dict(q=O + 4), -1), (dict(s=XS + 2), -1),
+    (dict(q=X), -1), (dict(q=X + 504), -1), (dict(s=X + 4), -1), (dict(s=O + 252), -1),
 ])
 def test_quantize_refusals(L, bad, want):
     assert quantize(L, **bad) == want
@@ -42,6 +43,7 @@ def fp8(L, x=X, xs=XS, w=W, ws=WS, T=4, N=64, K=64, bias=B, act=0, r=R, rd=1, ou
     (dict(T=(1 << 26) + 1), -2), (dict(x=None), -1), (dict(xs=None), -1), (dict(w=None), -1), (dict(ws=None), -1),
     (dict(out=None), -1), (dict(x=X + 8), -1), (dict(w=W + 4), -1), (dict(xs=XS + 2), -1), (dict(ws=WS + 1), -1),
     (dict(bias=B + 2), -1), (dict(out=O + 1), -1), (dict(r=R + 2), -1), (dict(r=O), -1), (dict(r=O + 2, rd=2), -1),
+    (dict(out=X), -1), (dict(out=W + 4094), -1), (dict(out=XS + 14), -1), (dict(out=WS), -1), (dict(out=B + 254), -1),
 ])
 def test_fp8_product_refusals(L, bad, want):
     assert fp8(L, **bad) == want
