@@ -46,8 +46,8 @@ inline size_t da_bytes(int64_t T, int64_t I) { return ((size_t)T * I * 4 + 255) 
 template <typename... S>
 moe_status grad_args(GradArgs& g, const uint16_t* dy, const uint16_t* x, const uint16_t* w, int32_t T, int32_t N,
                      int32_t K, void* dx, int32_t dx_dtype, void* dw, int32_t dw_dtype, int32_t accumulate, S... read) {
-  if (!float_dtype(dx_dtype) || !float_dtype(dw_dtype) || (!dx && !dw)) return MOE_ERR_INVALID_ARG;
-  if (T > 0 && (!dy || (dx && !w) || (dw && !x))) return MOE_ERR_INVALID_ARG;
+  if (!float_dtype(dx_dtype) || !float_dtype(dw_dtype)) return MOE_ERR_INVALID_ARG;
+  if (T > 0 && (!dy || (!dx && !dw) || (dx && !w) || (dw && !x))) return MOE_ERR_INVALID_ARG;
   if (!aligned(dy, 16) || !aligned(x, 16) || !aligned(w, 16) || !aligned(dx, 16) || !aligned(dw, 16))
     return MOE_ERR_INVALID_ARG;
   const Span sx{dw ? x : nullptr, (size_t)T * K * 2}, sw{dx ? w : nullptr, (size_t)N * K * 2};

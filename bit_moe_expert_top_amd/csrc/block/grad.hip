@@ -5,11 +5,13 @@
 // its way from LDS into the registers: ds_read_b64_tr_b16 gives lane i of 16 the i-th value of each of four rows of 16, of
 // which every lane points at four values; two of them make a lane's 8 k of one row of the operand.
 //
-// Both products of a call run in one launch: together they fill the GPU where one leaves places free.
-// Stages of SK (64 or 32) k in LDS, filled by direct global -> LDS loads: a row-major operand as rows of 128 bytes, its 16-byte chunks
-// XOR-swizzled by row / 2 as in moe_linear; a K-major one as 64 rows of its BM (or BN) values.  There a half wave reads 64
-// bytes of each of four rows, and these lie in different quarters of the banks where the chunks are XOR-swizzled by 4 (k % 4)
-// (rows of 256 bytes and more) or 4 (k / 2 % 2) (128 bytes).
+// Both products of a call run in one launch: together they fill the GPU where one leaves places free (1001 x 1008 x 2016: 14 us,
+// one after the other 25; 16384 x 2048 x 512: 76 and 91).
+// Stages of SK (64 or 32) k in LDS, filled by direct global -> LDS loads.  A row-major operand lies there as rows of 2 SK
+// bytes, its 16-byte chunks XOR-swizzled by row / 2 % 8 (row / 4 % 4 for SK = 32), so that one chunk of 16 consecutive rows
+// hits 16 bank groups; a K-major one as SK rows of its BM (or BN) values.  There a half wave reads 64 bytes of each of four
+// rows, and these lie in different quarters of the banks where the chunks are XOR-swizzled by 4 (k % 4) (rows of 256 bytes and
+// more) or 4 (k / 2 % 2) (128 bytes).
 // A step loads and waits without a branch: past the last k it loads zeros.  The rest is moe_linear's: the weight tile is the
 // MFMA's A operand, operands are read one sub-step of 16 k ahead, the sums pass through LDS in the epilogue.
 #include <algorithm>
@@ -45,7 +47,10 @@ struct Source {
   const uint8_t* base;
   int64_t ld;      // bytes from row to row as stored
   int rows;        // row-major: rows of the operand in the tile
-  __device__ static int swizzle(int row) { return KM ? (BR >= 128 ? 4 * (row & 3) : 4 * (row >> 1 & 1)) : SK == 64 ? row >> 1 & 7 : row >> 2 & 3; }
+  __device__ static int swizzle(int row) {
+    if (KM) return BR >= 128 ? 4 * (row & 3) : 4 * (row >> 1 & 1);
+    return SK == 64 ? row >> 1 & 7 : row >> 2 & 3;
+  }
   // row0: the tile's first row of the operand, of `total`; K: length of the sum
   __device__ void init(const uint8_t* p, int64_t row0, int64_t total, int K, int w, int lane) {
     const int r0 = lane / kChunks, c = lane % kChunks;
@@ -365,9 +370,9 @@ __global__ __launch_bounds__(256) void join_kernel(Join dx, Join dw) {
 // The parts of several splits are written and read once more in fp32, at about 5 TB/s and 4 us for the launch.
 // Not kept (us at 8192 x 4096, sums of 4096, and 4096 x 2048, sums of 8192, the kept ones 216 and 118): 256 x 128 in two
 // stages of 64 k 273 and 149; 256 x 256 in four stages of 32 k 219 and 173, by four waves with the sums in the
-// accumulation registers 220 and 174; 128 x 128 by four waves, two workgroups to a CU, 257 and 135.  Without the direct
-// loads 256 x 256 takes 178, without the operand reads 184: both pass through LDS, and their 256 KB a step take longer
-// there (1024 cycles for the loads' writes at 64 bytes a cycle, 1536 for the reads at 128) than the step's MFMAs (2048).
+// accumulation registers 220 and 174; 128 x 128 by four waves, two workgroups to a CU, 257 and 135.  What
+// bounds 256 x 256 is power: 8192 x 4096 with sums of 4096 takes 390 thousand cycles at 1.76 GHz (MFMAs alone: 262 thousand);
+// without the direct loads 378 at 1.91 GHz, without the operand reads 369 at 2.2: they are nearly hidden, but lower the clock.
 using Variant = GradVariant;
 using Plan = GradTiles;
 using Split = GradSplit;

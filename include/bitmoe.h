@@ -488,7 +488,7 @@ moe_status moe_glu(const uint16_t* x, const uint16_t* w, int32_t T, int32_t I, i
  *     dx = dy W,   dw = dy^T x  (added to what dw holds if accumulate)
  *   dy bf16 [T][N], x bf16 [T][K], w bf16 [N][K]
  *   dx    [T][K] of dx_dtype (F32 or BF16), or NULL (then w may be NULL)
- *   dw    [N][K] of dw_dtype (F32 or BF16), or NULL (then x may be NULL); not both NULL
+ *   dw    [N][K] of dw_dtype (F32 or BF16), or NULL (then x may be NULL); not both NULL unless T = 0
  *   ws    moe_linear_backward_ws_bytes(T, N, K) bytes, 16-byte aligned (fp32 parts of long sums of few outputs; NULL where
  *         it is 0)
  * Sums are fp32 on the matrix cores, rounded once; the same call gives the same bits.  T = 0 leaves dw zero (or, with

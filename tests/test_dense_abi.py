@@ -97,6 +97,8 @@ def test_of_no_rows(L):
     assert quantize(L, rows=0, x=None, q=None, s=None) == 0
     assert fp8(L, T=0, x=None, xs=None, w=None, ws=None, out=None) == 0
     assert glu(L, T=0, x=None, w=None, h=None) == 0
+    assert linear_backward(L, T=0, dy=None, x=None, w=None, dx=None, dw=None, ws=None, n=0) == 0
+    assert glu_backward(L, T=0, dh=None, a=None, x=None, w=None, dx=None, dw=None, ws=None, n=0) == 0
 
 
 def test_workspace_sizes(L):

@@ -350,7 +350,7 @@ def test_linear_backward_types_and_accumulation(L, dx, dw):
             check_linear_backward(L, T, N, K, dx=dx, dw=dw, accumulate=accumulate)
 
 
-def test_linear_backward_of_no_rows(L):
+def test_calls_of_no_rows(L):
     e = lambda *shape: torch.empty(shape, dtype=torch.bfloat16, device="cuda")
     for dtype in (torch.float32, torch.bfloat16):
         dw = torch.full((24, 40), 3.0, dtype=dtype, device="cuda")
@@ -361,6 +361,16 @@ def test_linear_backward_of_no_rows(L):
         dw.fill_(3.0)
         dx, _ = L.moe_glu_backward(e(0, 12 * 8), e(0, 24 * 8), e(0, 40), e(24 * 8, 40), dw=torch.ones(24 * 8, 40, device="cuda"))
         assert dx.shape == (0, 40)
+    # dx alone: nothing to do
+    assert L.moe_linear_backward(e(0, 24), None, e(24, 40), need_dw=False)[0].shape == (0, 40)
+    assert L.moe_glu_backward(e(0, 24), e(0, 48), None, e(48, 40), need_dw=False)[0].shape == (0, 40)
+    for act in ACTS:
+        assert L.moe_glu(e(0, 64), e(48, 64), act=act).shape == (0, 24)
+    q, s = L.moe_fp8_quantize(e(0, 272))
+    w, ws = L.moe_fp8_quantize(torch.randn(40, 272, device="cuda"), 128)
+    assert q.shape == (0, 272) and s.shape == (0, 3) and L.moe_linear_fp8(q, s, w, ws).shape == (0, 40)
+    q, s = L.moe_fp8_quantize(e(0, 272), block_rows=128)
+    assert q.shape == (0, 272) and s.shape == (0, 3)
 
 
 def test_linear_backward_needs(L):
