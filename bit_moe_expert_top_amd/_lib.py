@@ -538,30 +538,45 @@ def moe_glu(x: torch.Tensor, w: torch.Tensor, act: str = "silu", a=None, out=Non
     return out
 
 
-def _grad_outputs(fn: str, T: int, N: int, K: int, dev, x, w, dx, dw, need_dx, need_dw, accumulate):
-    """The arguments of a gradient call from x to accumulate, and the outputs; those that are not needed are None."""
+_ANY_FLOAT = tuple(_FLOAT_DT)
+
+
+def _grad_outputs(fn: str, T: int, N: int, K: int, dev, dx, dw, need_dx, need_dw, accumulate):
+    """The outputs of a gradient call, None where not needed, and their arguments."""
     if accumulate and dw is None:
         raise ValueError(f"{fn}: accumulate adds to a dw that is given")
-    if not need_dx and not need_dw:
-        raise ValueError(f"{fn}: expected need_dx or need_dw")
-    if dx is None and need_dx:
-        dx = torch.empty((T, K), dtype=torch.int16, device=dev)
-    if dw is None and need_dw:
-        dw = torch.empty((N, K), dtype=torch.int16, device=dev)
-    dx, dw = dx if need_dx else None, dw if need_dw else None
-    kind = lambda t: MOE_DT_BF16 if t is None else _FLOAT_DT.get(t.dtype, 0)
-    any_float = tuple(_FLOAT_DT)
-    return dx, dw, (_arg(x, _BF16, (T, K), dev, "x"), _arg(w, _BF16, (N, K), dev, "w")), (
-        _arg(dx, any_float, (T, K), dev, "dx"), kind(dx), _arg(dw, any_float, (N, K), dev, "dw"), kind(dw),
-        1 if accumulate else 0)
+    px = pw = None
+    kx = kw = MOE_DT_BF16
+    if not need_dx:
+        dx = None
+    else:
+        if dx is None:
+            dx = torch.empty((T, K), dtype=torch.int16, device=dev)
+        px = _arg(dx, _ANY_FLOAT, (T, K), dev, "dx")
+        kx = _FLOAT_DT[dx.dtype]
+    if not need_dw:
+        dw = None
+    else:
+        if dw is None:
+            dw = torch.empty((N, K), dtype=torch.int16, device=dev)
+        pw = _arg(dw, _ANY_FLOAT, (N, K), dev, "dw")
+        kw = _FLOAT_DT[dw.dtype]
+    return dx, dw, (px, kx, pw, kw, 1 if accumulate else 0)
 
 
 def _grad_ws(ws, need: int, dev):
-    """The workspace of a gradient call, and its size in bytes."""
+    """The workspace of a gradient call (None where it needs none), its pointer and its size in bytes."""
     if ws is None:
+        if need == 0:
+            return None, None, 0
         ws = torch.empty(need, dtype=torch.uint8, device=dev)
     _require(ws.dim() == 1, "ws", "a 1-d uint8 tensor")
     return ws, _arg(ws, (torch.uint8,), ws.shape, dev, "ws"), ws.numel()
+
+
+def _grad_needs(fn: str, ok: bool, x, w, need_dx, need_dw, of: str):
+    if not ok or not (need_dx or need_dw) or (need_dw and x is None) or (need_dx and w is None):
+        raise ValueError(f"{fn}: expected {of}, need_dx or need_dw, x for dw and w for dx")
 
 
 def moe_linear_backward(dy: torch.Tensor, x, w, dx=None, dw=None, need_dx: bool = True, need_dw: bool = True,
@@ -571,13 +586,13 @@ def moe_linear_backward(dy: torch.Tensor, x, w, dx=None, dw=None, need_dx: bool 
     operand that only it reads may be.  ws: moe_linear_backward_ws_bytes bytes, allocated if not given.
     Returns (dx, dw)."""
     dev = dy.device
-    if dy.dim() != 2 or (need_dw and x is None) or (need_dx and w is None):
-        raise ValueError("moe_linear_backward: expected dy [T][N], x for dw and w for dx")
+    _grad_needs("moe_linear_backward", dy.dim() == 2, x, w, need_dx, need_dw, "dy [T][N]")
     (T, N), K = dy.shape, (x if w is None else w).shape[-1]
     _sizes("moe_linear_backward", T | N | K, T, N, K)
-    dx, dw, operands, outs = _grad_outputs("moe_linear_backward", T, N, K, dev, x, w, dx, dw, need_dx, need_dw, accumulate)
+    dx, dw, outs = _grad_outputs("moe_linear_backward", T, N, K, dev, dx, dw, need_dx, need_dw, accumulate)
     ws, pws, n = _grad_ws(ws, lib.moe_linear_backward_ws_bytes(T, N, K), dev)
-    _call_on(dev, "moe_linear_backward", _arg(dy, _BF16, (T, N), dev, "dy"), *operands, T, N, K, *outs, pws, n)
+    _call_on(dev, "moe_linear_backward", _arg(dy, _BF16, (T, N), dev, "dy"), _arg(x, _BF16, (T, K), dev, "x"),
+             _arg(w, _BF16, (N, K), dev, "w"), T, N, K, *outs, pws, n)
     return dx, dw
 
 
@@ -586,14 +601,13 @@ def moe_glu_backward(dh: torch.Tensor, a: torch.Tensor, x, w, act: str = "silu",
     """The gradients of moe_glu from that of its output dh [T][I] and the pre-activations a [T][2I] it kept: dx [T][K]
     and dw [2I][K].  The rest as moe_linear_backward.  Returns (dx, dw)."""
     dev, code = dh.device, _glu_act("moe_glu_backward", act)
-    if dh.dim() != 2 or (need_dw and x is None) or (need_dx and w is None):
-        raise ValueError("moe_glu_backward: expected dh [T][I], x for dw and w for dx")
+    _grad_needs("moe_glu_backward", dh.dim() == 2, x, w, need_dx, need_dw, "dh [T][I]")
     (T, I), K = dh.shape, (x if w is None else w).shape[-1]
     _sizes("moe_glu_backward", T | I | K, T, I, K)
-    dx, dw, operands, outs = _grad_outputs("moe_glu_backward", T, 2 * I, K, dev, x, w, dx, dw, need_dx, need_dw, accumulate)
+    dx, dw, outs = _grad_outputs("moe_glu_backward", T, 2 * I, K, dev, dx, dw, need_dx, need_dw, accumulate)
     ws, pws, n = _grad_ws(ws, lib.moe_glu_backward_ws_bytes(T, I, K), dev)
-    _call_on(dev, "moe_glu_backward", _arg(dh, _BF16, (T, I), dev, "dh"), _arg(a, _BF16, (T, 2 * I), dev, "a"), *operands,
-             T, I, K, code, *outs, pws, n)
+    _call_on(dev, "moe_glu_backward", _arg(dh, _BF16, (T, I), dev, "dh"), _arg(a, _BF16, (T, 2 * I), dev, "a"),
+             _arg(x, _BF16, (T, K), dev, "x"), _arg(w, _BF16, (2 * I, K), dev, "w"), T, I, K, code, *outs, pws, n)
     return dx, dw
 
 

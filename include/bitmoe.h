@@ -490,7 +490,7 @@ moe_status moe_glu(const uint16_t* x, const uint16_t* w, int32_t T, int32_t I, i
  *   dx    [T][K] of dx_dtype (F32 or BF16), or NULL (then w may be NULL)
  *   dw    [N][K] of dw_dtype (F32 or BF16), or NULL (then x may be NULL); not both NULL unless T = 0
  *   ws    moe_linear_backward_ws_bytes(T, N, K) bytes, 16-byte aligned (fp32 parts of long sums of few outputs; NULL where
- *         it is 0)
+ *         it is 0); no other call may use it until this one has run
  * Sums are fp32 on the matrix cores, rounded once; the same call gives the same bits.  T = 0 leaves dw zero (or, with
  * accumulate, as it is).  No output may overlap an input, the other output or the workspace.
  * The order of a row's sums may follow the sizes.  moe_linear_backward_ws_bytes is 0 also for sizes that the call refuses.
