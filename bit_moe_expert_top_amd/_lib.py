@@ -373,6 +373,7 @@ SCORES = {"softmax": 1, "sigmoid": 2}
 # scales as bytes or as tensors of those types, where this torch has them
 _FLOAT_DT = {torch.float32: MOE_DT_F32, torch.bfloat16: MOE_DT_BF16, torch.int16: MOE_DT_BF16}
 _BF16 = (torch.bfloat16, torch.int16)
+_F32 = (torch.float32,)
 _E4M3 = tuple(getattr(torch, t) for t in ("uint8", "float8_e4m3fn") if hasattr(torch, t))
 _E8M0 = tuple(getattr(torch, t) for t in ("uint8", "float8_e8m0fnu") if hasattr(torch, t))
 
@@ -479,16 +480,19 @@ def moe_linear(x: torch.Tensor, w: torch.Tensor, x_scales=None, w_scales=None, b
 def moe_fp8_quantize(x: torch.Tensor, block_rows: int = 1, q=None, scales=None):
     """FP8 (e4m3) elements of x [rows][K] (fp32 or bf16) and their fp32 scales max|x| / 448, one for each block of
     block_rows (1: activations, 128: weights) x 128 values.  Returns (q, scales)."""
-    dev = x.device
-    if x.dim() != 2 or block_rows not in (1, 128) or x.dtype not in _FLOAT_DT:
+    dev, kind = x.device, _FLOAT_DT.get(x.dtype)
+    if kind is None or x.dim() != 2 or block_rows not in (1, 128):
         raise ValueError("moe_fp8_quantize: expected x [rows][K], fp32 or bf16, and block_rows 1 or 128")
-    rows, K = x.shape
-    _sizes("moe_fp8_quantize", rows | K, rows, K)
-    grid = ((rows + block_rows - 1) // block_rows, (K + 127) // 128)
-    q = torch.empty((rows, K), dtype=torch.uint8, device=dev) if q is None else q
-    scales = torch.empty(grid, dtype=torch.float32, device=dev) if scales is None else scales
-    _call_on(dev, "moe_fp8_quantize", _arg(x, (x.dtype,), (rows, K), dev, "x"), _FLOAT_DT[x.dtype], rows, K, block_rows,
-             _arg(q, _E4M3, (rows, K), dev, "q"), _arg(scales, (torch.float32,), grid, dev, "scales"))
+    rows, K = shape = x.shape
+    if (rows | K) >> 31:
+        _sizes("moe_fp8_quantize", rows | K, rows, K)
+    grid = (rows if block_rows == 1 else (rows + 127) // 128, (K + 127) // 128)
+    if q is None:
+        q = torch.empty(shape, dtype=torch.uint8, device=dev)
+    if scales is None:
+        scales = torch.empty(grid, dtype=torch.float32, device=dev)
+    _call_on(dev, "moe_fp8_quantize", _arg(x, _FLOAT_DT, shape, dev, "x"), kind, rows, K, block_rows,
+             _arg(q, _E4M3, shape, dev, "q"), _arg(scales, _F32, grid, dev, "scales"))
     return q, scales
 
 
@@ -497,24 +501,28 @@ def moe_linear_fp8(x: torch.Tensor, x_scales: torch.Tensor, w: torch.Tensor, w_s
     """out = act(x W^T + bias) + residual in bf16, x [T][K] and w [N][K] FP8 elements with fp32 scales as
     moe_fp8_quantize makes them (block_rows 1 and 128; swiglu: gate and up quantised apart and stacked, elements and
     scales).  The rest as moe_linear."""
-    dev = x.device
-    if x.dim() != 2 or w.dim() != 2 or act not in ACTS:
+    dev, code = x.device, ACTS.get(act)
+    if code is None or x.dim() != 2 or w.dim() != 2:
         raise ValueError(f"moe_linear_fp8: expected x [T][K], w [N][K] and an act of {sorted(ACTS)}")
     T, K = x.shape
     N = w.shape[0]
-    _sizes("moe_linear_fp8", T | N | K, T, N, K)
-    gated = act == "swiglu"
-    cols, kb = (N // 2 if gated else N), (K + 127) // 128
-    blocks = (cols + 127) // 128 * (2 if gated else 1)
+    if (T | N | K) >> 31:
+        _sizes("moe_linear_fp8", T | N | K, T, N, K)
+    kb = (K + 127) // 128
+    if act == "swiglu":
+        cols = N // 2
+        blocks = (cols + 127) // 128 * 2
+    else:
+        cols, blocks = N, (N + 127) // 128
     if out is None:
         out = torch.empty((T, cols), dtype=torch.int16, device=dev)
     pr, rd = None, MOE_DT_F32
     if residual is not None:
-        pr, rd = _arg(residual, tuple(_FLOAT_DT), (T, cols), dev, "residual"), _FLOAT_DT[residual.dtype]
-    _call_on(dev, "moe_linear_fp8", _arg(x, _E4M3, (T, K), dev, "x"),
-             _arg(x_scales, (torch.float32,), (T, kb), dev, "x_scales"), _arg(w, _E4M3, (N, K), dev, "w"),
-             _arg(w_scales, (torch.float32,), (blocks, kb), dev, "w_scales"), T, N, K,
-             _arg(bias, (torch.float32,), (N,), dev, "bias"), ACTS[act], pr, rd, _arg(out, _BF16, (T, cols), dev, "out"))
+        pr, rd = _arg(residual, _FLOAT_DT, (T, cols), dev, "residual"), _FLOAT_DT[residual.dtype]
+    _call_on(dev, "moe_linear_fp8", _arg(x, _E4M3, (T, K), dev, "x"), _arg(x_scales, _F32, (T, kb), dev, "x_scales"),
+             _arg(w, _E4M3, (N, K), dev, "w"), _arg(w_scales, _F32, (blocks, kb), dev, "w_scales"), T, N, K,
+             None if bias is None else _arg(bias, _F32, (N,), dev, "bias"), code, pr, rd,
+             _arg(out, _BF16, (T, cols), dev, "out"))
     return out
 
 
@@ -531,10 +539,12 @@ def moe_glu(x: torch.Tensor, w: torch.Tensor, act: str = "silu", a=None, out=Non
     if x.dim() != 2 or w.dim() != 2 or w.shape[0] % 2:
         raise ValueError("moe_glu: expected x [T][K] and w [2I][K]")
     (T, K), I = x.shape, w.shape[0] // 2
-    _sizes("moe_glu", T | I | K, T, I, K)
-    out = torch.empty((T, I), dtype=torch.int16, device=dev) if out is None else out
+    if (T | I | K) >> 31:
+        _sizes("moe_glu", T | I | K, T, I, K)
+    if out is None:
+        out = torch.empty((T, I), dtype=torch.int16, device=dev)
     _call_on(dev, "moe_glu", _arg(x, _BF16, (T, K), dev, "x"), _arg(w, _BF16, (2 * I, K), dev, "w"), T, I, K, code,
-             _arg(a, _BF16, (T, 2 * I), dev, "a"), _arg(out, _BF16, (T, I), dev, "out"))
+             None if a is None else _arg(a, _BF16, (T, 2 * I), dev, "a"), _arg(out, _BF16, (T, I), dev, "out"))
     return out
 
 

@@ -52,10 +52,10 @@ struct LinearArgs {
   int T, N, K;
   int n_out;  // N, or N/2 with a gate
   int act;
-  int glu_act;    // kActGlu: the gate's activation, and where the pre-activations go ([T][2 n_out], or nullptr)
-  uint16_t* pre;
   int res_f32, out_f32;
   int vec;  // rows of out, residual and pre allow 4-column vector accesses
+  int glu_act;    // kActGlu: the gate's activation, and where the pre-activations go ([T][2 n_out], or nullptr)
+  uint16_t* pre;
 };
 // few token rows (linear_rows.hip): 16 tt of them to a workgroup, tt = 1, 2 or 4
 hipError_t launch_linear_rows(const LinearArgs& a, LinearKind kind, int tt, hipStream_t s);

@@ -646,3 +646,54 @@ def test_block_captured(L):
         want = L.block_forward(blk, x, eager)
         torch.cuda.synchronize()
         assert torch.equal(got, want["out"]) and torch.equal(res, eager)
+
+
+# ------------------------------------------------------------------ types, differences
+def test_types_of_the_tensors(L):
+    """bf16 as its bits and e4m3 elements as that type: the same bits."""
+    r = np.random.default_rng(5)
+    x, w = bf16(r, 70, 144), bf16(r, 2 * 40, 144, scale=1 / 12)
+    q, s = L.moe_fp8_quantize(x)
+    q2, s2 = L.moe_fp8_quantize(x.view(torch.int16), q=torch.empty(70, 144, dtype=torch.float8_e4m3fn, device="cuda"))
+    assert torch.equal(q, q2.view(torch.uint8)) and torch.equal(s, s2)
+    wq, ws = L.moe_fp8_quantize(w, 128)
+    out = L.moe_linear_fp8(q, s, wq, ws)
+    same = L.moe_linear_fp8(q2, s, wq.view(torch.float8_e4m3fn), ws, out=torch.empty(70, 80, dtype=torch.bfloat16, device="cuda"))
+    assert out.dtype == torch.int16 and torch.equal(out, same.view(torch.int16))
+    a = torch.empty(70, 80, dtype=torch.int16, device="cuda")
+    h = L.moe_glu(x.view(torch.int16), w, a=a)
+    a2 = torch.empty(70, 80, dtype=torch.bfloat16, device="cuda")
+    assert torch.equal(h, L.moe_glu(x, w.view(torch.int16), a=a2)) and torch.equal(a, a2.view(torch.int16))
+    dx, dw = L.moe_glu_backward(h, a, x, w)
+    ex, ew = L.moe_glu_backward(h.view(torch.bfloat16), a2, x.view(torch.int16), w.view(torch.int16),
+                                dx=torch.empty(70, 144, dtype=torch.bfloat16, device="cuda"))
+    assert torch.equal(dx, ex.view(torch.int16)) and torch.equal(dw, ew)
+
+
+@pytest.mark.parametrize("T,I,K", [(9, 24, 40), (130, 72, 136)])
+def test_glu_gradient_against_differences(L, T, I, K):
+    """Without an activation h is quadratic in x and in w, so central differences have no error of their own: the
+    change of sum(dh h) along a direction is the gradient's product with it."""
+    r = np.random.default_rng([T, I])
+    grid = lambda *s: cuda(r.integers(-8, 9, size=s) / 8.0, torch.bfloat16)  # sums and differences are bf16 values again
+    x, w, ex, ew, dh = grid(T, K), grid(2 * I, K), grid(T, K), grid(2 * I, K), grid(T, I)
+    a = torch.empty(T, 2 * I, dtype=torch.bfloat16, device="cuda")
+    L.moe_glu(x, w, act="none", a=a)
+    dx, dw = L.moe_glu_backward(dh, a, x, w, act="none", dx=torch.empty(T, K, device="cuda"),
+                                dw=torch.empty(2 * I, K, device="cuda"))
+    d = values(dh)
+    for grad, e, of in ((dx, ex, lambda s: L.moe_glu(x + s * ex, w, act="none")),
+                        (dw, ew, lambda s: L.moe_glu(x, w + s * ew, act="none"))):
+        hi, lo = values(of(1)), values(of(-1))
+        want, got = float(((hi - lo) * d).sum()) / 2, float((values(grad) * values(e)).sum())
+        # h is rounded to bf16, the kept a and the gradient of a too: a 2^-8 of each term of the sums
+        av, ev = values(a), values(e)
+        if e is ex:
+            moved = np.abs(ev) @ np.abs(values(w)).T
+        else:
+            moved = np.abs(values(x)) @ np.abs(ev).T
+        terms = np.abs(d) * (np.abs(av[:, I:]) * moved[:, :I] + np.abs(av[:, :I]) * moved[:, I:])
+        bound = 2.0**-8 * ((np.abs(hi) + np.abs(lo)) * np.abs(d)).sum() / 2 + 2 * 2.0**-8 * terms.sum() * 1.01
+        assert abs(want - got) <= bound
+        # and much nearer where the roundings, being independent, cancel
+        assert abs(want - got) <= 8 * 2.0**-8 * (np.sqrt((((np.abs(hi) + np.abs(lo)) * d) ** 2).sum()) + np.sqrt((terms**2).sum()))
