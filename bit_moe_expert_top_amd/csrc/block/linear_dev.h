@@ -122,7 +122,8 @@ __device__ __forceinline__ FourBias load_bias4(const LinearArgs& a, int n) {
 }
 
 // What becomes of the weight rows' halves: kPlain no halves, kSwiglu silu(gate) * up, kGlu act(gate) * up with the
-// activation a.glu_act and, where a.pre is given, the pre-activations stored (rounded to bf16) for the backward pass.
+// activation a.glu_act and, where a.pre is given, the pre-activations stored (rounded to bf16) for the backward pass
+// (non-temporally in the larger tiles: 8192 x 4096 x 4096 229 -> 225 us, as fast as without them).
 constexpr int kPlain = 0, kSwiglu = 1, kGlu = 2;
 
 // Four bf16 values to p, of which cols lie inside the row.

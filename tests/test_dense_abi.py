@@ -25,7 +25,7 @@ def quantize(L, x=X, dt=2, rows=4, K=64, by=1, q=O, s=XS):
 
 @pytest.mark.parametrize("bad,want", [
     (dict(rows=-1), -1), (dict(K=0), -1), (dict(dt=3), -1), (dict(dt=0), -1), (dict(by=0), -1), (dict(by=64), -1),
-    (dict(K=72), -2), (dict(K=(1 << 20) + 16), -2), (dict(rows=(1 << 26) + 1), -2), (dict(x=None), -1), (dict(q=None), -1),
+    (dict(K=72), -2), (dict(K=(1 << 20) + 16), -2), (dict(rows=(1 << 26) + 1), -2), (dict(rows=1 << 26, K=4096), -2), (dict(x=None), -1), (dict(q=None), -1),
     (dict(s=None), -1), (dict(x=X + 8), -1), (dict(q=O + 4), -1), (dict(s=XS + 2), -1),
     (dict(q=X), -1), (dict(q=X + 504), -1), (dict(s=X + 4), -1), (dict(s=O + 252), -1),
 ])
