@@ -24,14 +24,14 @@ inline bool overlap(const void* a, size_t an, const void* b, size_t bn) {
   const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
   return x < y + bn && y < x + an;
 }
-// a, of which nothing has to be kept apart if it is null, shares bytes with any of the others
+// a shares bytes with any of the others; null and empty arrays have none
 struct Span {
   const void* p;
   size_t bytes;
 };
 template <typename... S>
 inline bool shares(Span a, S... others) {
-  return a.p && ((others.p && overlap(a.p, a.bytes, others.p, others.bytes)) || ...);
+  return a.p && a.bytes && ((others.p && others.bytes && overlap(a.p, a.bytes, others.p, others.bytes)) || ...);
 }
 inline bool float_dtype(int32_t d) { return d == MOE_DT_F32 || d == MOE_DT_BF16; }
 
@@ -42,10 +42,11 @@ inline bool grad_sizes(int32_t T, int32_t N, int32_t K) {
 inline size_t da_bytes(int64_t T, int64_t I) { return ((size_t)T * I * 4 + 255) / 256 * 256; }
 
 // Checks and fills what both gradient calls share.  dy: [T][N] (the gated call's lies in its workspace); read: the
-// other inputs and the workspace, which no output may share bytes with.
+// other inputs.  No output and no byte of the workspace may be an input's or another output's.
 template <typename... S>
 moe_status grad_args(GradArgs& g, const uint16_t* dy, const uint16_t* x, const uint16_t* w, int32_t T, int32_t N,
-                     int32_t K, void* dx, int32_t dx_dtype, void* dw, int32_t dw_dtype, int32_t accumulate, S... read) {
+                     int32_t K, void* dx, int32_t dx_dtype, void* dw, int32_t dw_dtype, int32_t accumulate, Span ws,
+                     S... read) {
   if (!float_dtype(dx_dtype) || !float_dtype(dw_dtype)) return MOE_ERR_INVALID_ARG;
   if (T > 0 && (!dy || (!dx && !dw) || (dx && !w) || (dw && !x))) return MOE_ERR_INVALID_ARG;
   if (!aligned(dy, 16) || !aligned(x, 16) || !aligned(w, 16) || !aligned(dx, 16) || !aligned(dw, 16))
@@ -53,7 +54,8 @@ moe_status grad_args(GradArgs& g, const uint16_t* dy, const uint16_t* x, const u
   const Span sx{dw ? x : nullptr, (size_t)T * K * 2}, sw{dx ? w : nullptr, (size_t)N * K * 2};
   const Span sdx{dx, (size_t)T * K * (dx_dtype == MOE_DT_F32 ? 4 : 2)};
   const Span sdw{dw, (size_t)N * K * (dw_dtype == MOE_DT_F32 ? 4 : 2)};
-  if (shares(sdx, sx, sw, sdw, read...) || shares(sdw, sx, sw, read...)) return MOE_ERR_INVALID_ARG;
+  if (shares(sdx, sx, sw, sdw, read...) || shares(sdw, sx, sw, read...) || shares(ws, sx, sw, sdx, sdw, read...))
+    return MOE_ERR_INVALID_ARG;
   g.dy = dy;
   g.x = x;
   g.w = w;
@@ -254,7 +256,7 @@ moe_status moe_linear_backward(const uint16_t* dy, const uint16_t* x, const uint
   if (!grad_sizes(T, N, K)) return MOE_ERR_UNSUPPORTED;
   GradArgs g{};
   const Span sdy{dy, (size_t)T * N * 2}, sws{ws, ws_bytes};
-  const moe_status bad = grad_args(g, dy, x, w, T, N, K, dx, dx_dtype, dw, dw_dtype, accumulate, sdy, sws);
+  const moe_status bad = grad_args(g, dy, x, w, T, N, K, dx, dx_dtype, dw, dw_dtype, accumulate, sws, sdy);
   if (bad != MOE_OK) return bad;
   const GradPlan plan = plan_grad(g);
   if (ws_bytes < plan.ws_bytes) return MOE_ERR_WORKSPACE;
@@ -275,9 +277,8 @@ moe_status moe_glu_backward(const uint16_t* dh, const uint16_t* a, const uint16_
   GradArgs g{};
   uint16_t* da = static_cast<uint16_t*>(ws);
   const Span sdh{dh, (size_t)T * I * 2}, sa{a, (size_t)T * I * 4}, sws{ws, ws_bytes};
-  const moe_status bad = grad_args(g, da, x, w, T, 2 * I, K, dx, dx_dtype, dw, dw_dtype, accumulate, sdh, sa, sws);
+  const moe_status bad = grad_args(g, da, x, w, T, 2 * I, K, dx, dx_dtype, dw, dw_dtype, accumulate, sws, sdh, sa);
   if (bad != MOE_OK) return bad;
-  if (T > 0 && shares(sws, sdh, sa)) return MOE_ERR_INVALID_ARG;
   const GradPlan plan = plan_grad(g);
   const size_t need = da_bytes(T, I) + plan.ws_bytes;
   if (ws_bytes < need) return MOE_ERR_WORKSPACE;

@@ -492,7 +492,7 @@ moe_status moe_glu(const uint16_t* x, const uint16_t* w, int32_t T, int32_t I, i
  *   ws    moe_linear_backward_ws_bytes(T, N, K) bytes, 16-byte aligned (fp32 parts of long sums of few outputs; NULL where
  *         it is 0); no other call may use it until this one has run
  * Sums are fp32 on the matrix cores, rounded once; the same call gives the same bits.  T = 0 leaves dw zero (or, with
- * accumulate, as it is).  No output may overlap an input, the other output or the workspace.
+ * accumulate, as it is).  No output and no byte of the workspace may overlap an input or one another.
  * The order of a row's sums may follow the sizes.  moe_linear_backward_ws_bytes is 0 also for sizes that the call refuses.
  * Errors: INVALID_ARG (bad sizes, types or pointers; a pointer not 16-byte aligned; overlaps), WORKSPACE (ws_bytes too
  * small), UNSUPPORTED (N or K % 8 != 0, N or K > 2^20, T > 2^26). */

@@ -93,6 +93,13 @@ def test_glu_backward_refusals(L, bad, want):
     assert glu_backward(L, **bad) == want
 
 
+@pytest.mark.parametrize("call", [linear_backward, glu_backward])
+@pytest.mark.parametrize("ws", [X, W, D, X + 256, W - (1 << 21), DX, DW])
+def test_workspace_apart(L, call, ws):
+    """The workspace is written before or while the inputs are read: it may share bytes with no array."""
+    assert call(L, ws=ws) == -1
+
+
 def test_of_no_rows(L):
     assert quantize(L, rows=0, x=None, q=None, s=None) == 0
     assert fp8(L, T=0, x=None, xs=None, w=None, ws=None, out=None) == 0
