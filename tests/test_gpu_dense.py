@@ -67,7 +67,7 @@ def check_quantize(L, x, by):
     want_q, want_s = OD.fp8_quantize(host(x.float()), by)
     np.testing.assert_array_equal(host(s), want_s)  # NaN counts as equal
     got = host(q)
-    # a zero's sign is free
+    # a zero's sign has a test of its own
     np.testing.assert_array_equal(np.where(got == 0x80, 0, got), np.where(want_q == 0x80, 0, want_q))
     assert guard_kept(qbuf) and guard_kept(sbuf)
 
@@ -115,6 +115,19 @@ def test_quantize_extremes(L, by):
             x = np.repeat(x, 128, axis=0)
             x[1::128] *= 0.5
         check_quantize(L, cuda(x, dtype), by)
+
+
+@pytest.mark.parametrize("by", [1, 128])
+@pytest.mark.parametrize("top", [2.0**-100, 1.0, 2.0**110])
+def test_quantize_signed_zeros(L, by, top):
+    """-0 and negative values that round to zero are 0x80, with the short division and with the plain one."""
+    v = np.tile([0.0, -0.0, 2.0**-20, -(2.0**-20)], (4, 32))
+    v[:, 5] = 1.0
+    x = cuda(v * top)
+    q, _ = L.moe_fp8_quantize(x, block_rows=by)
+    want = np.tile([0x00, 0x80, 0x00, 0x80], (4, 32))
+    want[:, 5] = 0x7E  # 448
+    np.testing.assert_array_equal(host(q), want)
 
 
 # ------------------------------------------------------------------ FP8 product
