@@ -2,7 +2,8 @@
 // weights) on v_mfma_f32_16x16x128_f8f6f4, whose K is a block: with the tokens' scale a[t][b] and the weights' c[n][b]
 //   sum[t][n] = sum over blocks b of a[t][b] c[n][b] p_b,   p_b = sum over the block's k of x[t][k] w[n][k]
 // so one instruction gives p_b of 16 x 16 outputs, from zero, and one fp32 FMA a value adds it with both scales.
-// A lane holds four outputs of one token and one block of weight rows, so the scale is one product a token tile.
+// A lane holds four outputs of one token and one block of weight rows, so the scale is one product a token tile.  Scales
+// whose products may leave the range of fp32 are told on the way, and the tile's sums made again (see scale_range).
 // The FMAs of a token tile stand between the MFMAs of the next one, on the other pipe (8192 x 4096 x 4096 on 256 x 256
 // tiles: 121 us, without the FMAs 108, without the direct loads 105; MFMAs alone would take 64 at the clock of 2.06 GHz that
 // they leave: the LDS traffic of a step, 128 bytes a cycle, takes as long as its MFMAs).
@@ -44,6 +45,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void linear_fp8_kernel(LinearArgs 
   // one object per stage: the compiler tracks direct loads per object
   __shared__ __align__(16) uint8_t st0[kStage], st1[kStage], st2[S == 4 ? kStage : 16], st3[S == 4 ? kStage : 16];
   __shared__ float sc0[kThreads], sc1[kThreads], sc2[S == 4 ? kThreads : 4], sc3[S == 4 ? kThreads : 4];
+  __shared__ uint32_t far_of[NW];  // whether a wave has met scales out of range
   const int tid = threadIdx.x, lane = wave_lane(), r16 = lane & 15, g = lane >> 4;
   const int w = __builtin_amdgcn_readfirstlane(tid / kWave), wm = w % WM, wn = w / WM;
   const int K = a.K, nk = (K + kRow - 1) / kRow;
@@ -114,9 +116,11 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void linear_fp8_kernel(LinearArgs 
     __builtin_amdgcn_raw_ptr_buffer_load_lds(is_x ? rx : rw, (lds_void*)dst, 16, (int)(in ? off : kOffNone), kb * kRow, 0, 0);
   };
   // the scales of stage kb into buffer d
+  uint32_t range = 0, put = 0;  // of the scales met (see scale_range), and the last one
   auto put_scales = [&](int d, int kb) {
     const int i = kb - group(kb / 4);
-    scales(d)[tid] = __uint_as_float(i == 0 ? sreg[0] : i == 1 ? sreg[1] : i == 2 ? sreg[2] : sreg[3]);
+    put = i == 0 ? sreg[0] : i == 1 ? sreg[1] : i == 2 ? sreg[2] : sreg[3];
+    scales(d)[tid] = __uint_as_float(put);
   };
 
   // a lane's two chunks of a row: the swizzle has a period of 16 rows, so they are the same for every tile
@@ -161,6 +165,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void linear_fp8_kernel(LinearArgs 
       if (d < S - 1 || i * kSpread * BT / LD < BT) load_one(d, d, i);
   wait_vm<(S - 2) * LD + LD / kSpread, false>();
   put_scales(0, 0);
+  range = scale_range(range, put);
   wait_vm<63, true>();
   asm volatile("s_barrier" ::: "memory");
 #pragma unroll
@@ -196,6 +201,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void linear_fp8_kernel(LinearArgs 
         add(t == 0 ? AT - 1 : t - 1, b);
         tmp[b] = mfma_fp8_16x16x128(wv[b][0], wv[b][1], xv[t & 1][0], xv[t & 1][1], f32x4{0.f, 0.f, 0.f, 0.f});
         keep(tmp[b]);
+        if (t == 0 && b == 0) range = scale_range(range, put);  // behind an MFMA (in front 1 % slower)
         if (last) read_w(next, b);
         // the refill of a stage is spread over the last token tile of its step and the first ones of the next
         const int part = (t + 1) % AT * BT + b, fd = last ? d : (d + S - 1) % S, fk = last ? kb + S : kb - 1 + S;
@@ -224,6 +230,8 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void linear_fp8_kernel(LinearArgs 
 #pragma unroll
   for (int b = 0; b < BT; ++b) add(AT - 1, b);
   wait_vm<0, true>();
+  const bool wave_far = __ballot(far_scales(range)) != 0;
+  if (lane == 0) far_of[w] = wave_far;
 
   // ---- epilogue: 32 token rows of the wave at a time pass through the wave's part of the stages (rows of 16 BT sums and
   // a pad of four), then a lane takes four consecutive columns, so that a store covers whole lines of a row.  The residual
@@ -245,6 +253,46 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void linear_fp8_kernel(LinearArgs 
   };
   fetch(0);
   __syncthreads();  // all waves have read the last stage
+  uint32_t any_far = 0;
+#pragma unroll
+  for (int i = 0; i < NW; ++i) any_far |= far_of[i];
+  if (__builtin_amdgcn_readfirstlane(any_far) != 0) {
+    // the sums once more, a stage at a time, with the scales taken apart (see scale_range)
+#pragma unroll
+    for (int t = 0; t < AT; ++t)
+#pragma unroll
+      for (int b = 0; b < BT; ++b) acc[t][b] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll 1
+    for (int k = 0; k < nk; ++k) {
+#pragma unroll
+      for (int i = 0; i < LD; ++i) load_one(0, k, i);
+      load_scales(k / 4);
+      put_scales(0, k);
+      wait_vm<0, true>();
+      asm volatile("s_barrier" ::: "memory");
+      read_sw(0);
+      SplitScale cw[NS];
+#pragma unroll
+      for (int h = 0; h < NS; ++h) cw[h] = split_scale(sw[h]);
+#pragma unroll
+      for (int t = 0; t < AT; ++t) {
+        read_x(0, t, 0);
+        const SplitScale cx = split_scale(sx[0]);
+#pragma unroll
+        for (int b = 0; b < BT; ++b) {
+          const SplitScale& c = cw[GATED ? b & 1 : 0];
+          read_w(0, b);
+          tmp[b] = mfma_fp8_16x16x128(wv[b][0], wv[b][1], xv[0][0], xv[0][1], f32x4{0.f, 0.f, 0.f, 0.f}, c.e, cx.e);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) acc[t][b][i] = fmaf(cx.m * c.m, tmp[b][i], acc[t][b][i]);
+          keep(acc[t][b]);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      wait_vm<0, true>();
+      asm volatile("s_barrier" ::: "memory");
+    }
+  }
   constexpr int kFit = kStage / (32 * kPitch * 4);  // waves whose part fits one stage
   static_assert(kFit > 0 && (NW + kFit - 1) / kFit <= S, "epilogue staging");
   float* ep = reinterpret_cast<float*>(stage(w / kFit)) + w % kFit * 32 * kPitch;

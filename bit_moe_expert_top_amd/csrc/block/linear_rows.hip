@@ -16,6 +16,8 @@
 // v_mfma_f32_16x16x128_f8f6f4 without scales for FP8: a run of 128 bytes is one block of K, and its sum is added with both
 // fp32 scales (1 x 4096 x 4096 SwiGLU 5.2 us, 64 x 4096 x 4096 9.9 us a launch).
 // Lane l receives output rows (weight rows) 4 (l / 16) + i of token column l % 16.
+#include <type_traits>
+
 #include "linear_dev.h"
 
 namespace bitmoe {
@@ -119,7 +121,8 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void linear_rows_kernel(LinearArgs
   uint32_t wpos[2], xpos[2];
   chunks(r16, wpos);
   chunks(r16 % XR, xpos);
-  auto compute = [&](int u) {
+  uint32_t range = 0;  // FP8: of the scales met
+  auto compute = [&](int u, auto apart) {
     const uint8_t* st = slot(u);
     u32x4 wv[2], xv[TT][2];
 #pragma unroll
@@ -141,12 +144,29 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void linear_rows_kernel(LinearArgs
       }
     } else if constexpr (FP8) {
       // a run is one block of K: its sum by itself, then times both scales into the fp32 sum
-      const float sw = __int_as_float(__builtin_amdgcn_ds_bpermute(4 * (4 * g), (int)sreg[u][0]));
+      auto scale = [&](int row, int c) {
+        return __int_as_float(__builtin_amdgcn_ds_bpermute(4 * row, (int)sreg[u][c]));
+      };
+      const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
+      const float sw = scale(4 * g, 0);
+      if constexpr (!decltype(apart)::value) {
+#pragma unroll
+        for (int c = 0; c < kSc; ++c) range = scale_range(range, sreg[u][c]);
+      }
 #pragma unroll
       for (int t = 0; t < TT; ++t) {
-        const int i = t + 1;
-        const float sc = sw * __int_as_float(__builtin_amdgcn_ds_bpermute(4 * (16 * (i % 4) + r16), (int)sreg[u][i / 4]));
-        const f32x4 p = mfma_fp8_16x16x128(wv[0], wv[1], xv[t][0], xv[t][1], f32x4{0.f, 0.f, 0.f, 0.f});
+        const float sx = scale(16 * ((t + 1) % 4) + r16, (t + 1) / 4);
+        float sc;
+        f32x4 p;
+        if constexpr (decltype(apart)::value) {
+          // the mantissa of the weight rows whose sums a lane receives, the power of two of the one that it supplies
+          const SplitScale cw = split_scale(sw), cx = split_scale(sx);
+          sc = cw.m * cx.m;
+          p = mfma_fp8_16x16x128(wv[0], wv[1], xv[t][0], xv[t][1], zero, split_scale(scale(r16, 0)).e, cx.e);
+        } else {
+          sc = sw * sx;
+          p = mfma_fp8_16x16x128(wv[0], wv[1], xv[t][0], xv[t][1], zero);
+        }
 #pragma unroll
         for (int j = 0; j < 4; ++j) acc[t][j] = fmaf(sc, p[j], acc[t][j]);
       }
@@ -159,33 +179,56 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void linear_rows_kernel(LinearArgs
     }
   };
   // runs w, w + NW, ...: U of them in flight
+  auto all_runs = [&](auto apart) {
 #pragma unroll
-  for (int u = 0; u < U; ++u)
-    if (w + NW * u < runs) load(u, w + NW * u);
-  for (int run = w; run < runs; run += NW * U) {
+    for (int u = 0; u < U; ++u)
+      if (w + NW * u < runs) load(u, w + NW * u);
+    for (int run = w; run < runs; run += NW * U) {
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int r = run + NW * u;
-      if (r >= runs) break;
-      if (r + NW * (U - 1) < runs)
-        wait_vm<(U - 1) * LD, false>();  // the U - 1 later runs may be in flight
-      else
-        wait_vm<0, false>();
-      asm volatile("" ::: "memory");
-      compute(u);
-      if (r + NW * U < runs) {
-        wait_vm<63, true>();  // this wave's reads of the slot are done
+      for (int u = 0; u < U; ++u) {
+        const int r = run + NW * u;
+        if (r >= runs) break;
+        if (r + NW * (U - 1) < runs)
+          wait_vm<(U - 1) * LD, false>();  // the U - 1 later runs may be in flight
+        else
+          wait_vm<0, false>();
         asm volatile("" ::: "memory");
-        load(u, r + NW * U);
+        compute(u, apart);
+        if (r + NW * U < runs) {
+          wait_vm<63, true>();  // this wave's reads of the slot are done
+          asm volatile("" ::: "memory");
+          load(u, r + NW * U);
+        }
       }
     }
-  }
-  __syncthreads();
+  };
   float* part = reinterpret_cast<float*>(s0);  // [NW][TT][64][4]
+  auto put_parts = [&] {
+    __syncthreads();  // all waves have read their slots
 #pragma unroll
-  for (int t = 0; t < TT; ++t)
-    *reinterpret_cast<float4*>(part + ((w * TT + t) * 64 + lane) * 4) = make_float4(acc[t][0], acc[t][1], acc[t][2], acc[t][3]);
-  __syncthreads();
+    for (int t = 0; t < TT; ++t)
+      *reinterpret_cast<float4*>(part + ((w * TT + t) * 64 + lane) * 4) = make_float4(acc[t][0], acc[t][1], acc[t][2], acc[t][3]);
+    __syncthreads();
+  };
+  all_runs(std::false_type{});
+  if constexpr (FP8) {
+    __shared__ uint32_t far_of[NW];
+    const bool wave_far = __ballot(far_scales(range)) != 0;
+    if (lane == 0) far_of[w] = wave_far;
+    put_parts();
+    uint32_t any_far = 0;
+#pragma unroll
+    for (int i = 0; i < NW; ++i) any_far |= far_of[i];
+    if (__builtin_amdgcn_readfirstlane(any_far) != 0) {
+      // the sums once more with the scales taken apart (see scale_range)
+#pragma unroll
+      for (int t = 0; t < TT; ++t) acc[t] = f32x4{0.f, 0.f, 0.f, 0.f};
+      all_runs(std::true_type{});
+      put_parts();
+    }
+  } else {
+    put_parts();
+  }
   if (w >= TT) return;
   float v[4] = {0.f, 0.f, 0.f, 0.f}, u[4];
 #pragma unroll

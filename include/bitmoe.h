@@ -466,7 +466,8 @@ moe_status moe_fp8_quantize(const void* x, int32_t x_dtype, int64_t rows, int32_
  *   bias, act, residual, residual_dtype   as moe_linear
  *   out            bf16 [T][N, or N/2 with SwiGLU]; may be a bf16 residual itself
  * A block's products are summed by the FP8 matrix cores (not an fp32 sum: see moe_linear), the blocks in fp32.  The order
- * of a row's sums may follow T, so its bits may change with the batch size.
+ * of a row's sums may follow T, so its bits may change with the batch size.  Scales are any fp32 values; the product of
+ * two may leave the range of fp32 where a block's part of the sum does not.
  * Errors: INVALID_ARG (bad sizes, types or pointers; N odd with SwiGLU; x or w not 16-byte aligned; out over part of
  * residual or over another operand), UNSUPPORTED (K % 16 != 0; N or K > 2^20; T > 2^26). */
 moe_status moe_linear_fp8(const uint8_t* x, const float* x_scales, const uint8_t* w, const float* w_scales, int32_t T,

@@ -257,6 +257,72 @@ def test_fp8_rows_do_not_touch_each_other(L):
             target[T // 2] = old
 
 
+# token rows and weight rows, one for each kernel of the product (few rows: 8, 16, 32 and 64 to a slot; tiles of 64, of 128
+# with one and two workgroups to a CU, of 256)
+FP8_KERNELS = [(1, 96), (12, 96), (30, 4090), (60, 4096), (200, 2050), (520, 4090), (1100, 4090), (2100, 4090)]
+
+
+@pytest.mark.parametrize("T,N", FP8_KERNELS)
+@pytest.mark.parametrize("size,power", [("small", 132), ("large", -145), ("large", -153)])
+@pytest.mark.parametrize("act", ["none", "swiglu"])
+def test_fp8_scales_whose_product_leaves_fp32(L, T, N, size, power, act):
+    """x_scale * w_scale is about 2^power, beyond the range of fp32 or where it has few bits left; the results are not.
+    With SwiGLU so for the up rows, and gates near 1."""
+    r = np.random.default_rng([T, abs(power)])
+    K, kb = 4 * 128 + 48, 5
+
+    def elements(n):
+        # of both signs: the smallest magnitude and zeros, or the largest magnitudes
+        q = r.integers(0, 2, size=(n, K)) if size == "small" else r.integers(0x78, 0x7F, size=(n, K))
+        return (q | 0x80 * r.integers(0, 2, size=(n, K))).astype(np.uint8)
+
+    def scales(n, e):
+        return (r.uniform(1, 2, size=(n, kb)) * 2.0**e).astype(np.float32)
+
+    # the blocks share the power between the sides differently, with subnormal scales among them
+    ex = 66 + np.array([0, 20, -10, 10, 7]) if power > 0 else -75 + np.array([0, 20, -15, -60, 7])
+    x, xs, w = elements(T), scales(T, ex), elements(N)
+    if act == "swiglu":
+        near = 15 if size == "small" else -20  # the sums of products are about 2^-near
+        ws = np.concatenate([scales(OD.up(N // 2), near - ex), scales(OD.up(N // 2), power - ex)])
+    else:
+        ws = scales(OD.up(N), power - ex)
+    xv, wv = OD.fp8_values(x, xs, 1), OD.fp8_values(w, ws, 128, act == "swiglu")
+    want = OB.linear(xv, wv, act_name=act)
+    got = values(L.moe_linear_fp8(*(torch.from_numpy(t).cuda() for t in (x, xs, w, ws)), act=act))
+    # as in check_fp8; where results are subnormal, half a step of bf16 there, and a step of fp32 for each operation before
+    a = OB.linear(xv, wv)
+    dev = KAPPA * np.sqrt((xv * xv) @ (wv * wv).T) + (kb + 3) * 2.0**-23 * (np.abs(xv) @ np.abs(wv).T) + 4 * kb * 2.0**-149
+    dev = act_deviation(a, dev, act, N // 2)
+    dev = dev + (np.abs(want) + dev) * 2.0**-8 + 2.0**-134 + 2.0**-148
+    assert 2.0**-133 < np.abs(want).max() < 2.0**127
+    np.testing.assert_array_less(np.abs(got - want), dev * 1.0001)
+
+
+@pytest.mark.parametrize("T,N", FP8_KERNELS)
+def test_fp8_zero_sums_under_huge_scales(L, T, N):
+    """A block whose products are all zero adds nothing, however large the (finite) scales of both sides are."""
+    r = np.random.default_rng(T)
+    x, w = r.integers(0, 0x7F, size=(T, 272)).astype(np.uint8), r.integers(0, 0x7F, size=(N, 272)).astype(np.uint8)
+    x[:, :128], w[:, 128:] = 0, 0
+    xs, ws = np.full((T, 3), 2.0**100, dtype=np.float32), np.full((OD.up(N), 3), 2.0**100, dtype=np.float32)
+    got = L.moe_linear_fp8(*(torch.from_numpy(t).cuda() for t in (x, xs, w, ws)))
+    assert not got.view(torch.bfloat16).float().abs().max().item()
+
+
+@pytest.mark.parametrize("T,N", FP8_KERNELS)
+def test_fp8_far_scale_of_one_row(L, T, N):
+    """A token row with a scale of 2^70 or 2^-70 changes no bit of the other rows, which are summed beside it."""
+    r = np.random.default_rng(T)
+    (x, xs, _), (w, ws, _) = fp8_operand(L, bf16(r, T, 272), 1), fp8_operand(L, bf16(r, N, 272), 128)
+    a = L.moe_linear_fp8(x, xs, w, ws)
+    keep = [t for t in range(T) if t != T // 2]
+    for power in (70, -70):
+        xs[T // 2] = 2.0**power
+        b = L.moe_linear_fp8(x, xs, w, ws)
+        assert torch.equal(a[keep], b[keep]) and not torch.equal(a[T // 2], b[T // 2])
+
+
 # ------------------------------------------------------------------ gated projection
 def check_glu(L, T, I, K, act, keep=True, scale=1.0):
     r = np.random.default_rng([T, I, K])
