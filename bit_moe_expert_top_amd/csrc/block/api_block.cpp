@@ -173,7 +173,9 @@ moe_status moe_linear(const void* x, const uint8_t* x_scales, const void* w, con
 moe_status moe_fp8_quantize(const void* x, int32_t x_dtype, int64_t rows, int32_t K, int32_t block_rows, uint8_t* q,
                             float* scales, void* stream) {
   if (rows < 0 || K < 1 || !float_dtype(x_dtype) || (block_rows != 1 && block_rows != 128)) return MOE_ERR_INVALID_ARG;
-  if (K % 16 || K > kMaxLinear || rows > kMaxLinearRows || rows * ((K + 127) / 128) >= (int64_t)1 << 31)
+  // blocks of a row and 128, or of 128 x 128: a launch has fewer than 2^32 threads
+  if (K % 16 || K > kMaxLinear || rows > kMaxLinearRows || rows * ((K + 127) / 128) >= (int64_t)1 << 31 ||
+      (block_rows == 128 && (rows + 127) / 128 * ((K + 127) / 128) >= 1 << 24))
     return MOE_ERR_UNSUPPORTED;
   if (rows == 0) return MOE_OK;
   if (!x || !q || !scales || !aligned(x, 16) || !aligned(q, 8) || !aligned(scales, 4)) return MOE_ERR_INVALID_ARG;

@@ -97,51 +97,50 @@ __global__ __launch_bounds__(kThreads) void quantize_rows_kernel(const XT* x, ui
   }
 }
 
-// A scale per 128 x 128 values: a workgroup to a block, a thread holds 16 values of 4 rows.
+// A scale per 128 x 128 values: a workgroup to a block (fewer than 2^24), a thread holds 16 values of 4 rows.
 template <typename XT>
 __global__ __launch_bounds__(kThreads) void quantize_blocks_kernel(const XT* x, int64_t rows, int K, int kb, uint8_t* q,
                                                                    float* scales) {
   constexpr int kPass = kThreads / kLanes, kPasses = 128 / kPass;  // rows of a pass
-  __shared__ uint32_t part[2][kThreads / kWave];
-  const int64_t blocks = (rows + 127) / 128 * kb;
-  int parity = 0;  // two buffers in turn: a wave may write the next block's part while another still reads this one's
-  for (int64_t b = blockIdx.x; b < blocks; b += gridDim.x, parity ^= 1) {
-    const int64_t rb = b / kb, r0 = 128 * rb + threadIdx.x / kLanes;
-    const int c = 128 * (int)(b - rb * kb) + 16 * (threadIdx.x % kLanes);
-    float v[kPasses][2][8];
-    uint32_t m = 0;
+  __shared__ uint32_t part[kThreads / kWave];
+  const uint32_t b = blockIdx.x, rb = b / (uint32_t)kb;
+  const int64_t r0 = 128 * (int64_t)rb + threadIdx.x / kLanes;
+  const int c = 128 * (int)(b - rb * (uint32_t)kb) + 16 * (threadIdx.x % kLanes);
+  float v[kPasses][2][8];
+  uint32_t m = 0;
 #pragma unroll
-    for (int i = 0; i < kPasses; ++i) {
+  for (int i = 0; i < kPasses; ++i) {
 #pragma unroll
-      for (int k = 0; k < 8; ++k) v[i][0][k] = v[i][1][k] = 0.f;
-      const XT* p = x + (r0 + kPass * i) * K + c;
-      if (c < K && r0 + kPass * i < rows) load8(p, v[i][0]), load8(p + 8, v[i][1]);
-      m = max(m, max(top8(v[i][0]), top8(v[i][1])));
-    }
-#pragma unroll
-    for (int off = 1; off < kWave; off <<= 1) m = max(m, (uint32_t)__shfl_xor((int)m, off));
-    if (wave_lane() == 0) part[parity][threadIdx.x / kWave] = m;
-    __syncthreads();
-#pragma unroll
-    for (int i = 0; i < kThreads / kWave; ++i) m = max(m, part[parity][i]);
-    const Scale sc = scale_of(m);
-#pragma unroll
-    for (int i = 0; i < kPasses; ++i)
-      if (c < K && r0 + kPass * i < rows) store16(q + (r0 + kPass * i) * K + c, v[i], sc);
-    if (threadIdx.x == 0) scales[b] = sc.s;
+    for (int k = 0; k < 8; ++k) v[i][0][k] = v[i][1][k] = 0.f;
+    const XT* p = x + (r0 + kPass * i) * K + c;
+    if (c < K && r0 + kPass * i < rows) load8(p, v[i][0]), load8(p + 8, v[i][1]);
+    m = max(m, max(top8(v[i][0]), top8(v[i][1])));
   }
+#pragma unroll
+  for (int off = 1; off < kWave; off <<= 1) m = max(m, (uint32_t)__shfl_xor((int)m, off));
+  if (wave_lane() == 0) part[threadIdx.x / kWave] = m;
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < kThreads / kWave; ++i) m = max(m, part[i]);
+  const Scale sc = scale_of(m);
+#pragma unroll
+  for (int i = 0; i < kPasses; ++i)
+    if (c < K && r0 + kPass * i < rows) store16(q + (r0 + kPass * i) * K + c, v[i], sc);
+  if (threadIdx.x == 0) scales[b] = sc.s;
 }
 
 template <typename XT>
 hipError_t go(const XT* x, int64_t rows, int K, int by, uint8_t* q, float* scales, hipStream_t s) {
   const int kb = (K + 127) / 128;
-  const int64_t blocks = (by == 1 ? rows : (rows + 127) / 128) * kb;
-  const int64_t want = by == 1 ? (blocks + kThreads / kLanes - 1) / (kThreads / kLanes) : blocks;
-  const unsigned grid = (unsigned)(want < (1 << 20) ? want : 1 << 20);
-  if (by == 1)
+  if (by == 1) {
+    // a workgroup takes more than one turn from 2^25 blocks on (a launch has fewer than 2^32 threads; with 2^16 workgroups
+    // at most 131072 x 4096 bf16 takes 286 instead of 277 us)
+    const int64_t blocks = rows * kb, want = (blocks + kThreads / kLanes - 1) / (kThreads / kLanes);
+    const unsigned grid = (unsigned)(want < (1 << 20) ? want : 1 << 20);
     quantize_rows_kernel<XT><<<grid, kThreads, 0, s>>>(x, (uint32_t)blocks, K, kb, q, scales);
-  else
-    quantize_blocks_kernel<XT><<<grid, kThreads, 0, s>>>(x, rows, K, kb, q, scales);
+  } else {
+    quantize_blocks_kernel<XT><<<(unsigned)((rows + 127) / 128 * kb), kThreads, 0, s>>>(x, rows, K, kb, q, scales);
+  }
   return hipGetLastError();
 }
 

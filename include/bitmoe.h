@@ -452,7 +452,7 @@ moe_status moe_route_scored(const float* logits, const float* bias, int32_t T, i
  * block's scale infinite (its own element NaN, the others 0), a NaN makes scale and elements NaN.
  * Errors: INVALID_ARG (bad sizes, types or pointers; x not 16-byte, q not 8-byte, scales not 4-byte aligned; arrays that
  * overlap),
- * UNSUPPORTED (K % 16 != 0; K > 2^20; rows > 2^26; 2^31 blocks of 128 in all rows or more). */
+ * UNSUPPORTED (K % 16 != 0; K > 2^20; rows > 2^26; 2^31 blocks of 128 in all rows or more, 2^24 of 128 x 128). */
 moe_status moe_fp8_quantize(const void* x, int32_t x_dtype, int64_t rows, int32_t K, int32_t block_rows, uint8_t* q,
                             float* scales, void* stream);
 

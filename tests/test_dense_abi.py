@@ -33,6 +33,13 @@ def test_quantize_refusals(L, bad, want):
     assert quantize(L, **bad) == want
 
 
+@pytest.mark.parametrize("rows,by,want", [(1 << 18, 1, -2), ((1 << 18) - 1, 128, -2), ((1 << 18) - 127, 128, -2),
+                                          ((1 << 18) - 128, 128, -1), ((1 << 18) - 1, 1, -1)])
+def test_quantize_block_counts(L, rows, by, want):
+    """The largest counts of blocks: below them the call gets as far as the missing arrays."""
+    assert quantize(L, x=None, rows=rows, K=1 << 20, by=by) == want
+
+
 def fp8(L, x=X, xs=XS, w=W, ws=WS, T=4, N=64, K=64, bias=B, act=0, r=R, rd=1, out=O):
     return L.lib.moe_linear_fp8(x, xs, w, ws, T, N, K, bias, act, r, rd, out, None)
 

@@ -95,6 +95,22 @@ def test_quantize_many_blocks(L, by):
     np.testing.assert_array_equal(host(s[blocks]), want_s)
 
 
+@pytest.mark.parametrize("rows,K,by,dtype", [
+    ((1 << 25) + 77, 16, 1, torch.bfloat16),   # workgroups that take two turns: from 2^25 blocks on
+    (1 << 26, 16, 1, torch.bfloat16),          # all of them do, and the largest number of rows
+    ((1 << 24) + 33, 144, 1, torch.float32),
+    (128 * 16384 + 5, 144, 128, torch.bfloat16),
+])
+def test_quantize_large_is_its_slices(L, rows, K, by, dtype):
+    """A call of many blocks has the bits of calls of 2^20 rows each."""
+    x = torch.randn(rows, K, device="cuda", dtype=dtype)
+    q, s = L.moe_fp8_quantize(x, block_rows=by)
+    for i in range(0, rows, 1 << 20):
+        part = x[i:i + (1 << 20)]
+        pq, ps = L.moe_fp8_quantize(part, block_rows=by)
+        assert torch.equal(q[i:i + (1 << 20)], pq) and torch.equal(s[i // by:i // by + len(ps)], ps), i
+
+
 @pytest.mark.parametrize("by", [1, 128])
 def test_quantize_extremes(L, by):
     """Zeros, subnormal and huge values, ties, infinities and NaN, each in a block of its own."""
