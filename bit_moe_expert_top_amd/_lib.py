@@ -75,6 +75,7 @@ _SIGS = {
     "moe_linear_backward": (_i32, [_p] * 3 + [_i32] * 3 + [_p, _i32, _p, _i32, _i32, _p, _sz, _p]),
     "moe_glu_backward_ws_bytes": (_sz, [_i32] * 3),
     "moe_glu_backward": (_i32, [_p] * 4 + [_i32] * 4 + [_p, _i32, _p, _i32, _i32, _p, _sz, _p]),
+    "moe_debug_grad_tiles": (_i32, [_i32] * 4 + [ctypes.POINTER(_i32)]),
     "moe_status_str": (ctypes.c_char_p, [_i32]),
     "moe_tier_plan": (_i32, [ctypes.POINTER(MoeTierState), _p, _i64, _p, _p, _p]),
     "moe_tier_load": (_i32, [ctypes.POINTER(MoeWeights), ctypes.POINTER(MoeWeights), _p, _p, _i32, _p]),
@@ -619,6 +620,14 @@ def moe_glu_backward(dh: torch.Tensor, a: torch.Tensor, x, w, act: str = "silu",
     _call_on(dev, "moe_glu_backward", _arg(dh, _BF16, (T, I), dev, "dh"), _arg(a, _BF16, (T, 2 * I), dev, "a"),
              _arg(x, _BF16, (T, K), dev, "x"), _arg(w, _BF16, (2 * I, K), dev, "w"), T, I, K, code, *outs, pws, n)
     return dx, dw
+
+
+def moe_debug_grad_tiles(T: int, N: int, K: int, need_dx: bool = True, need_dw: bool = True) -> dict:
+    """How a gradient call of these sizes is laid out: the tiles of dx (those of dw are turned round), the splits of
+    both sums, and whether dw's workgroups come first."""
+    v = (_i32 * 5)()
+    _check("moe_debug_grad_tiles", lib.moe_debug_grad_tiles(T, N, K, bool(need_dx) + 2 * bool(need_dw), v))
+    return dict(tile=(v[0], v[1]), splits_dx=v[2], splits_dw=v[3], dw_first=bool(v[4]))
 
 
 def moe_route_scored(logits: torch.Tensor, k: int, score: str = "softmax", bias=None, n_group: int = 1,

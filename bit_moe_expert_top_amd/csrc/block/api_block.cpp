@@ -266,6 +266,24 @@ moe_status moe_linear_backward(const uint16_t* dy, const uint16_t* x, const uint
   return from_hip(launch_grad(g, plan, ws, as_stream(stream)));
 }
 
+moe_status moe_debug_grad_tiles(int32_t T, int32_t N, int32_t K, int32_t which, int32_t* tiles) {
+  if (T < 1 || N < 1 || K < 1 || which < 1 || which > 3 || !tiles) return MOE_ERR_INVALID_ARG;
+  if (!grad_sizes(T, N, K)) return MOE_ERR_UNSUPPORTED;
+  GradArgs g{};
+  g.dx = which & 1 ? tiles : nullptr;  // only whether they are wanted counts here
+  g.dw = which & 2 ? tiles : nullptr;
+  g.T = T;
+  g.N = N;
+  g.K = K;
+  const GradTiles p = plan_grad(g).plan;
+  tiles[0] = p.tiles == kTile64 ? 64 : p.tiles == kTile256 ? 256 : 128;
+  tiles[1] = p.tiles == kTile64 ? 64 : p.tiles == kTile128 ? 128 : 256;
+  tiles[2] = p.dx.splits;
+  tiles[3] = p.dw.splits;
+  tiles[4] = p.dw_first;
+  return MOE_OK;
+}
+
 size_t moe_glu_backward_ws_bytes(int32_t T, int32_t I, int32_t K) {
   return I % 8 == 0 && I <= kMaxLinear / 2 && grad_sizes(T, 2 * I, K) ? da_bytes(T, I) + grad_ws_bytes(T, 2 * I, K) : 0;
 }

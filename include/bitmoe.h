@@ -524,6 +524,14 @@ moe_status moe_glu_backward(const uint16_t* dh, const uint16_t* a, const uint16_
 moe_status moe_debug_dequant(const moe_weights* w, int32_t e, int32_t which, float* out,
                              void* stream);
 
+/* moe_debug_grad_tiles -- how a gradient call of these sizes is laid out (N = 2I for moe_glu_backward): its tiles and the
+ * splits of its sums.  For tests: they ask that every layout is run.  Host only.
+ *   which   1 dx alone, 2 dw alone, 3 both
+ *   tiles   [5]: rows and columns of a tile of dx (those of dw turned round), splits of the sums of dx and of dw, and
+ *           whether the workgroups of dw come first
+ * Errors: INVALID_ARG, and UNSUPPORTED as the calls. */
+moe_status moe_debug_grad_tiles(int32_t T, int32_t N, int32_t K, int32_t which, int32_t* tiles);
+
 /* Human-readable name of a status code (static string). */
 const char* moe_status_str(moe_status s);
 

@@ -134,6 +134,28 @@ def test_workspace_sizes(L):
         assert L.lib.moe_glu_backward_ws_bytes(*bad) == 0
 
 
+@pytest.mark.parametrize("bad,want", [((0, 8, 8, 3), -1), ((4, 0, 8, 3), -1), ((4, 8, -8, 3), -1), ((4, 8, 8, 0), -1),
+                                      ((4, 8, 8, 4), -1), ((4, 12, 8, 3), -2), ((4, 8, 1 << 21, 3), -2)])
+def test_grad_tiles_refusals(L, bad, want):
+    import ctypes
+
+    v = (ctypes.c_int32 * 5)()
+    assert L.lib.moe_debug_grad_tiles(*bad, v) == want
+    assert L.lib.moe_debug_grad_tiles(4, 8, 8, 3, None) == -1
+
+
+def test_grad_tiles(L):
+    """What the layout says of the workspace: fp32 parts of the split sums, none without."""
+    assert L.moe_debug_grad_tiles(8192, 4096, 4096) == dict(tile=(256, 256), splits_dx=1, splits_dw=1, dw_first=True)
+    for T, N, K in ((16384, 512, 256), (3426, 200, 384), (1, 4096, 4096)):
+        parts = 0
+        for dx, dw in ((True, True), (True, False), (False, True)):
+            lay = L.moe_debug_grad_tiles(T, N, K, dx, dw)
+            n = (lay["splits_dx"] * T * K if lay["splits_dx"] > 1 else 0) + (lay["splits_dw"] * N * K if lay["splits_dw"] > 1 else 0)
+            parts = max(parts, 4 * n)
+        assert L.lib.moe_linear_backward_ws_bytes(T, N, K) == parts
+
+
 BF = torch.bfloat16
 
 

@@ -445,6 +445,87 @@ def test_linear_backward_types_and_accumulation(L, dx, dw):
             check_linear_backward(L, T, N, K, dx=dx, dw=dw, accumulate=accumulate)
 
 
+# sizes off every tile for each layout of a gradient call: gradients wanted, tile of dx, whether the sums of dx and of dw are
+# split, whether dw's workgroups come first
+GRAD_LAYOUTS = [
+    ((1001, 1008, 2016), "both", (128, 128), False, False, False),
+    ((471, 32, 3600), "both", (128, 128), False, False, True),
+    ((3426, 200, 384), "both", (128, 128), False, True, False),
+    ((7258, 32, 200), "both", (128, 128), False, True, True),
+    ((238, 3400, 328), "both", (128, 128), True, False, False),
+    ((260, 3984, 264), "both", (128, 128), True, False, True),
+    ((5845, 1752, 72), "both", (128, 128), True, True, False),
+    ((8214, 1024, 80), "both", (128, 128), True, True, True),
+    ((8243, 32, 216), "dx", (128, 128), False, False, False),
+    ((205, 720, 2696), "dw", (128, 128), False, False, True),
+    ((5131, 72, 2240), "dw", (128, 128), False, True, True),
+    ((341, 664, 3632), "both", (128, 256), False, False, False),
+    ((520, 416, 3832), "both", (128, 256), False, False, True),
+    ((3721, 200, 648), "both", (128, 256), False, True, False),
+    ((7308, 32, 464), "both", (128, 256), False, True, True),
+    ((206, 3792, 760), "both", (128, 256), True, False, False),
+    ((467, 3416, 728), "both", (128, 256), True, False, True),
+    ((8557, 920, 144), "both", (128, 256), True, True, True),
+    ((8490, 32, 416), "dx", (128, 256), False, False, False),
+    ((8191, 4088, 2040), "dw", (128, 256), False, False, True),
+    ((8580, 1480, 648), "dw", (128, 256), False, True, True),
+    ((919, 1088, 3984), "both", (256, 256), False, False, False),
+    ((8191, 4088, 2040), "both", (256, 256), False, False, True),
+    ((16381, 2040, 504), "both", (256, 256), False, True, False),
+    ((3408, 32, 2056), "both", (256, 256), False, True, True),
+    ((496, 3992, 1304), "both", (256, 256), True, False, False),
+    ((8631, 32, 800), "dx", (256, 256), False, False, False),
+    ((202, 3384, 2408), "dw", (256, 256), False, False, True),
+]
+
+
+@pytest.mark.parametrize("sizes,need,tile,split_dx,split_dw,dw_first", GRAD_LAYOUTS)
+def test_linear_backward_layouts(L, sizes, need, tile, split_dx, split_dw, dw_first):
+    """Every layout with tiles wider than 64, of both types and with accumulation, against fp64 products on the GPU."""
+    T, N, K = sizes
+    nx, nw = need != "dw", need != "dx"
+    lay = L.moe_debug_grad_tiles(T, N, K, nx, nw)
+    assert (lay["tile"], lay["splits_dx"] > 1, lay["splits_dw"] > 1, lay["dw_first"]) == (tile, split_dx, split_dw, dw_first)
+    gen = torch.Generator(device="cuda").manual_seed(T + N + K)
+    normal = lambda *shape, scale: (scale * torch.randn(*shape, generator=gen, device="cuda")).bfloat16()
+    dy, x, w = normal(T, N, scale=0.01), normal(T, K, scale=1.0), normal(N, K, scale=K**-0.5)
+    y64, x64, w64 = dy.double(), x.double(), w.double()
+    yt = y64.t().contiguous()
+    half = {"f32": 2.0**-24, "bf16": 2.0**-8}
+
+    def check(got, want, dev, dtype):
+        dev = (dev + (want.abs() + dev) * half[dtype]) * 1.0001 + 1e-37
+        assert bool(((got.double() - want).abs() <= dev).all()), (dtype, float(((got.double() - want).abs() / dev).max()))
+
+    if nx:
+        want_x, dev_x = y64 @ w64, min(N * 2.0**-23, 1e-3) * (y64.abs() @ w64.abs())
+    if nw:
+        want_w, dev_w = yt @ x64, min((T + 8) * 2.0**-23, 1e-3) * (yt.abs() @ x64.abs())
+    for tx, tw, accumulate in (("bf16", "bf16", False), ("f32", "f32", True), ("bf16", "f32", False), ("f32", "bf16", True)):
+        gx, xbuf = guarded((T, K), DT[tx]) if nx else (None, None)
+        gw, wbuf = guarded((N, K), DT[tw]) if nw else (None, None)
+        before = normal(N, K, scale=0.1)
+        if nw and accumulate:
+            gw.copy_(before)
+        L.moe_linear_backward(dy, x if nw else None, w if nx else None, dx=gx, dw=gw, need_dx=nx, need_dw=nw,
+                              accumulate=accumulate and nw)
+        torch.cuda.synchronize()
+        if nx:
+            check(gx, want_x, dev_x, tx)
+            assert guard_kept(xbuf)
+        if nw:
+            total = want_w + before.double() if accumulate else want_w
+            check(gw, total, dev_w + 2.0**-23 * total.abs() if accumulate else dev_w, tw)
+            assert guard_kept(wbuf)
+
+
+@pytest.mark.parametrize("T,I,K,tile", [(1001, 504, 2016, (128, 128)), (341, 336, 3632, (128, 256)), (919, 544, 3984, (256, 256))])
+def test_glu_backward_wide_tiles(L, T, I, K, tile):
+    assert L.moe_debug_grad_tiles(T, 2 * I, K)["tile"] == tile
+    for dw, accumulate in (("bf16", False), ("f32", True)):
+        check_glu_backward(L, T, I, K, "gelu", dw=dw, accumulate=accumulate)
+
+
 def test_calls_of_no_rows(L):
     e = lambda *shape: torch.empty(shape, dtype=torch.bfloat16, device="cuda")
     for dtype in (torch.float32, torch.bfloat16):
