@@ -575,9 +575,11 @@ def _grad_outputs(fn: str, T: int, N: int, K: int, dev, dx, dw, need_dx, need_dw
     return dx, dw, (px, kx, pw, kw, 1 if accumulate else 0)
 
 
-def _grad_ws(ws, need: int, dev):
-    """The workspace of a gradient call (None where it needs none), its pointer and its size in bytes."""
+def _grad_ws(ws, size, dev, *sizes):
+    """The workspace of a gradient call (None where it needs none), its pointer and its size in bytes.  One that is
+    given is not sized here: size(*sizes) lays out the call three times (dx, dw, both), the call itself once more."""
     if ws is None:
+        need = size(*sizes)
         if need == 0:
             return None, None, 0
         ws = torch.empty(need, dtype=torch.uint8, device=dev)
@@ -601,7 +603,7 @@ def moe_linear_backward(dy: torch.Tensor, x, w, dx=None, dw=None, need_dx: bool 
     (T, N), K = dy.shape, (x if w is None else w).shape[-1]
     _sizes("moe_linear_backward", T | N | K, T, N, K)
     dx, dw, outs = _grad_outputs("moe_linear_backward", T, N, K, dev, dx, dw, need_dx, need_dw, accumulate)
-    ws, pws, n = _grad_ws(ws, lib.moe_linear_backward_ws_bytes(T, N, K), dev)
+    ws, pws, n = _grad_ws(ws, lib.moe_linear_backward_ws_bytes, dev, T, N, K)
     _call_on(dev, "moe_linear_backward", _arg(dy, _BF16, (T, N), dev, "dy"), _arg(x, _BF16, (T, K), dev, "x"),
              _arg(w, _BF16, (N, K), dev, "w"), T, N, K, *outs, pws, n)
     return dx, dw
@@ -616,7 +618,7 @@ def moe_glu_backward(dh: torch.Tensor, a: torch.Tensor, x, w, act: str = "silu",
     (T, I), K = dh.shape, (x if w is None else w).shape[-1]
     _sizes("moe_glu_backward", T | I | K, T, I, K)
     dx, dw, outs = _grad_outputs("moe_glu_backward", T, 2 * I, K, dev, dx, dw, need_dx, need_dw, accumulate)
-    ws, pws, n = _grad_ws(ws, lib.moe_glu_backward_ws_bytes(T, I, K), dev)
+    ws, pws, n = _grad_ws(ws, lib.moe_glu_backward_ws_bytes, dev, T, I, K)
     _call_on(dev, "moe_glu_backward", _arg(dh, _BF16, (T, I), dev, "dh"), _arg(a, _BF16, (T, 2 * I), dev, "a"),
              _arg(x, _BF16, (T, K), dev, "x"), _arg(w, _BF16, (2 * I, K), dev, "w"), T, I, K, code, *outs, pws, n)
     return dx, dw

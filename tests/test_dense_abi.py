@@ -156,6 +156,16 @@ def test_grad_tiles(L):
         assert L.lib.moe_linear_backward_ws_bytes(T, N, K) == parts
 
 
+def test_given_workspace_is_not_sized(L):
+    ws = torch.empty(64, dtype=torch.uint8)
+    asked = []
+    size = lambda *sizes: asked.append(sizes) or 32
+    assert L._grad_ws(ws, size, ws.device, 1, 2, 3) == (ws, ws.data_ptr(), 64) and not asked
+    got = L._grad_ws(None, size, ws.device, 1, 2, 3)
+    assert got[0].shape == (32,) and got[1:] == (got[0].data_ptr(), 32) and asked == [(1, 2, 3)]
+    assert L._grad_ws(None, lambda: 0, ws.device) == (None, None, 0)
+
+
 BF = torch.bfloat16
 
 
