@@ -53,7 +53,7 @@ struct LinearArgs {
   int n_out;  // N, or N/2 with a gate
   int act;
   int res_f32, out_f32;
-  int vec;  // rows of out, residual and pre allow 4-column vector accesses
+  int vec;  // rows of out and residual allow 4-column vector accesses (those of pre always do)
   int glu_act;    // kActGlu: the gate's activation, and where the pre-activations go ([T][2 n_out], or nullptr)
   uint16_t* pre;
 };

@@ -155,20 +155,14 @@ __device__ __forceinline__ FourBias load_bias4(const LinearArgs& a, int n) {
 // (non-temporally in the larger tiles: 8192 x 4096 x 4096 229 -> 225 us, as fast as without them).
 constexpr int kPlain = 0, kSwiglu = 1, kGlu = 2;
 
-// Four bf16 values to p, of which cols lie inside the row.
+// Four bf16 values to p, 8-byte aligned.
 template <bool STREAM>
-__device__ __forceinline__ void store_bf16x4(uint16_t* p, const float (&v)[4], bool vec, int cols) {
-  if (vec) {
-    const u32x2 q = {f32x2_to_bf16x2_rne(v[0], v[1]), f32x2_to_bf16x2_rne(v[2], v[3])};
-    if (STREAM)
-      __builtin_nontemporal_store(q, reinterpret_cast<u32x2*>(p));
-    else
-      *reinterpret_cast<u32x2*>(p) = q;
-    return;
-  }
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-    if (i < cols) p[i] = (uint16_t)f32_to_bf16_rne(v[i]);
+__device__ __forceinline__ void store_bf16x4(uint16_t* p, const float (&v)[4]) {
+  const u32x2 q = {f32x2_to_bf16x2_rne(v[0], v[1]), f32x2_to_bf16x2_rne(v[2], v[3])};
+  if (STREAM)
+    __builtin_nontemporal_store(q, reinterpret_cast<u32x2*>(p));
+  else
+    *reinterpret_cast<u32x2*>(p) = q;
 }
 
 // v (and, with a gate, the up columns u): the sums without bias.  Adds the bias, applies the
@@ -184,9 +178,9 @@ __device__ __forceinline__ void epilogue4(const LinearArgs& a, int64_t at, int n
   for (int i = 0; i < 4; ++i) r[i] = v[i] + bias.g[i];
   if constexpr (GATED == kGlu) {
     if (a.pre) {
-      uint16_t* gate = a.pre + 2 * at - n;  // row t of 2 n_out columns, at = t n_out + n
-      store_bf16x4<STREAM>(gate, v, a.vec, a.n_out - n);
-      store_bf16x4<STREAM>(gate + a.n_out, u, a.vec, a.n_out - n);
+      uint16_t* gate = a.pre + 2 * at - n;  // row t of 2 n_out columns, at = t n_out + n; n_out is a multiple of 8
+      store_bf16x4<STREAM>(gate, v);
+      store_bf16x4<STREAM>(gate + a.n_out, u);
     }
     activate(r, a.glu_act);
 #pragma unroll
