@@ -535,7 +535,8 @@ def _glu_act(fn: str, act: str) -> int:
 
 def moe_glu(x: torch.Tensor, w: torch.Tensor, act: str = "silu", a=None, out=None):
     """h = act(g) * u with [g | u] = x W^T; x [T][K] and w [2I][K] bf16, the gate's rows first.  a (bf16 [T][2I]),
-    if given, receives [g | u] for moe_glu_backward.  Returns h, bf16 [T][I]."""
+    if given, receives [g | u] for moe_glu_backward.  Returns h, bf16 [T][I].  Like every call here it is not recorded by
+    autograd: a training step makes the gradient calls itself."""
     dev, code = x.device, _glu_act("moe_glu", act)
     if x.dim() != 2 or w.dim() != 2 or w.shape[0] % 2:
         raise ValueError("moe_glu: expected x [T][K] and w [2I][K]")

@@ -1,5 +1,5 @@
 // C ABI of the operators around the expert FFN (declared in include/bitmoe.h): argument checks
-// and dispatch.  No allocation, no workspace, no host synchronisation.
+// and dispatch.  No allocation and no host synchronisation; a workspace only in the gradient calls, from the caller.
 #include <hip/hip_runtime.h>
 
 #include <cmath>

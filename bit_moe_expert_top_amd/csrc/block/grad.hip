@@ -368,6 +368,11 @@ __global__ __launch_bounds__(256) void join_kernel(Join dx, Join dw) {
 //   256 x 256, eight waves, two stages                    256        12.5   23.7
 // (The K-major operand is the wide one: rows of 32 k of the other are half a cache line.)
 // The parts of several splits are written and read once more in fp32, at about 5 TB/s and 4 us for the launch.
+// Sums below 1024 (few tokens) are outside these measurements, and the model there is only near: against every tile and split,
+// N x K = 4096 x 4096 and 4096 x 2048, 1 to 512 tokens, the chosen layout takes 12 to 18 % longer than the best for both products
+// (T = 1: 26.0 and 23.0 us, T = 64: 27.5 and 23.8, T = 512: 60.6 and 51.2, each the best with 128 x 128 tiles), up to 40 % for dx
+// alone (8 tokens: 12.7 and 9.1; 64 and more: at most 16 %), 2 % for dW alone; at 1024 x 2048 4 %.  (They take about twice their bytes' time
+// in any layout: one round of tiles with short sums is mostly fill and epilogue.)
 // Not kept (us at 8192 x 4096, sums of 4096, and 4096 x 2048, sums of 8192, the kept ones 216 and 118): 256 x 128 in two
 // stages of 64 k 273 and 149; 256 x 256 in four stages of 32 k 219 and 173, by four waves with the sums in the
 // accumulation registers 220 and 174; 128 x 128 by four waves, two workgroups to a CU, 257 and 135.  What

@@ -338,7 +338,7 @@ hipError_t go(const LinearArgs& a, hipStream_t s) {
 // (one or two to a CU).  The times of a round were measured at K = 4096 without a residual (us, back to back, buffers in
 // turn of three):
 //   token rows x weight rows                       at once    us
-//   16 x 16, 32 x 16, 64 x 16  (linear_rows)       256        5.8, 7.0, 9.8
+//   16 x 16, 32 x 16, 64 x 16  (linear_rows)       256        5.8, 7.0, 9.8  (6.0, 6.9, 9.4 with the test of the scales' range)
 //   64 x 64, four stages                           256        12.7
 //   64 x 64, four stages                           512        18.2
 //   128 x 128, eight waves, four stages            256        24

@@ -14,7 +14,8 @@
 // its 16-byte chunks c = 0, 1 and the e8m0 scale of the 32-k block l / 16.  (Its sums are not fp32 sums: see
 // mfma_mxfp8_32x32x64.)
 // v_mfma_f32_16x16x128_f8f6f4 without scales for FP8: a run of 128 bytes is one block of K, and its sum is added with both
-// fp32 scales (1 x 4096 x 4096 SwiGLU 5.2 us, 64 x 4096 x 4096 9.9 us a launch).
+// fp32 scales (1 x 4096 x 4096 SwiGLU 5.8 us, 64 x 4096 x 4096 9.4 us a launch); scales whose product may leave the range of
+// fp32 are told on the way, and the sums made again with them apart (see scale_range).
 // Lane l receives output rows (weight rows) 4 (l / 16) + i of token column l % 16.
 #include <type_traits>
 
