@@ -757,6 +757,44 @@ def test_two_graphs_and_another_stream(L):
                 assert torch.equal(b[k], w[k]), k
 
 
+def test_split_sums_captured(L):
+    """Gradients whose parts lie in a workspace, captured with one of their own and with a given one that holds NaN."""
+    r = np.random.default_rng(21)
+    for T, N, K in ((3426, 200, 384), (206, 3792, 760), (8214, 1024, 80)):
+        lay = L.moe_debug_grad_tiles(T, N, K)
+        assert lay["splits_dx"] > 1 or lay["splits_dw"] > 1
+        dy, x, w = bf16(r, T, N, scale=0.01), bf16(r, T, K), bf16(r, N, K, scale=K**-0.5)
+        dx, dw = torch.empty(T, K, device="cuda"), torch.zeros(N, K, device="cuda")
+        ws = torch.empty(L.lib.moe_linear_backward_ws_bytes(T, N, K) + 4096, dtype=torch.uint8, device="cuda")
+        graphs = []
+        for given in (None, ws):
+            g = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(g):
+                L.moe_linear_backward(dy, x, w, dx=dx, dw=dw, accumulate=True, ws=given)
+            graphs.append(g)
+        for i in range(3):
+            dy.copy_(bf16(r, T, N, scale=0.01))
+            want = L.moe_linear_backward(dy, x, w, dx=torch.empty_like(dx), dw=torch.ones_like(dw), accumulate=True)
+            torch.cuda.synchronize()
+            for g in graphs:
+                ws.fill_(0xFF)
+                dx.fill_(7)
+                dw.fill_(1)
+                g.replay()
+                torch.cuda.synchronize()
+                assert torch.equal(dx, want[0]) and torch.equal(dw, want[1]), (T, N, K, i)
+
+
+def test_gradients_of_one_tensor_twice(L):
+    """dy, x and w may be one array, or parts of one that overlap."""
+    r = np.random.default_rng(22)
+    big = bf16(r, 1000, 136)
+    for a, x, w in ((big[8:144], big[8:144], big[8:144]), (big[:700], big[16:716], big[3:139])):
+        dx, dw = L.moe_linear_backward(a, x, w)
+        ex, ew = L.moe_linear_backward(a.clone(), x.clone(), w.clone())
+        assert torch.equal(dx, ex) and torch.equal(dw, ew)
+
+
 def test_same_bits_on_every_call(L):
     for T in (3, 150, 700):
         run, b, _ = all_calls(L, T)
